@@ -42,6 +42,8 @@ EXPORTS = (
     "glq_workspace_info", "glq_workspace_release", "glq_layer_create_stages",
     "glq_layer_set_batch_invariant", "glq_layer_create_shard", "glq_cast",
     "glq_rht_input_operand", "glq_layer_selftest_wait",
+    "glq_fp8_quantize", "glq_fp8_create", "glq_fp8_destroy", "glq_fp8_reserve", "glq_fp8_linear",
+    "glq_fp8_linear_quantized", "glq_fp8_dequant", "glq_fp8_check", "glq_fp8_info",
 )
 
 
@@ -88,6 +90,15 @@ _SIGNATURES = {
                         ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
     "glq_workspace_info": ([_i32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
     "glq_workspace_release": ([_i32], ctypes.c_int),
+    "glq_fp8_quantize": ([_vp, ctypes.c_int, _i64, _i64, _vp, _vp, _vp], ctypes.c_int),
+    "glq_fp8_create": ([_i64, _i64, _vp, _i64, _vp, _vp, ctypes.POINTER(_vp)], ctypes.c_int),
+    "glq_fp8_destroy": ([_vp], ctypes.c_int),
+    "glq_fp8_reserve": ([_vp, _i64], ctypes.c_int),
+    "glq_fp8_linear": ([_vp, _vp, ctypes.c_int, _vp, ctypes.c_int, _i64, _vp], ctypes.c_int),
+    "glq_fp8_linear_quantized": ([_vp, _vp, _vp, _vp, ctypes.c_int, _i64, _vp], ctypes.c_int),
+    "glq_fp8_dequant": ([_vp, _vp, _vp], ctypes.c_int),
+    "glq_fp8_check": ([_vp, _vp], ctypes.c_int),
+    "glq_fp8_info": ([_vp, ctypes.POINTER(_i64), ctypes.POINTER(_i64), ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
 }
 
 _lib = None
@@ -323,6 +334,46 @@ def glq_layer_info(handle):
     return m.value, n.value, bpw.value, nb.value
 
 
+def glq_fp8_quantize(x_ptr, x_dtype, B, n, q_ptr, s_ptr, stream) -> None:
+    _ok(_L().glq_fp8_quantize(x_ptr, x_dtype, B, n, q_ptr, s_ptr, stream), "glq_fp8_quantize")
+
+
+def glq_fp8_create(m, n, w_ptr, ldw, scales_ptr, stream) -> int:
+    h = _vp()
+    _ok(_L().glq_fp8_create(m, n, w_ptr, ldw, scales_ptr, stream, ctypes.byref(h)), "glq_fp8_create")
+    return h.value
+
+
+def glq_fp8_destroy(handle: int) -> None:
+    _ok(_L().glq_fp8_destroy(handle), "glq_fp8_destroy")
+
+
+def glq_fp8_reserve(handle: int, max_B: int) -> None:
+    _ok(_L().glq_fp8_reserve(handle, max_B), "glq_fp8_reserve")
+
+
+def glq_fp8_linear(handle, x_ptr, x_dtype, y_ptr, y_dtype, B, stream) -> None:
+    _ok(_L().glq_fp8_linear(handle, x_ptr, x_dtype, y_ptr, y_dtype, B, stream), "glq_fp8_linear")
+
+
+def glq_fp8_linear_quantized(handle, q_ptr, s_ptr, y_ptr, y_dtype, B, stream) -> None:
+    _ok(_L().glq_fp8_linear_quantized(handle, q_ptr, s_ptr, y_ptr, y_dtype, B, stream), "glq_fp8_linear_quantized")
+
+
+def glq_fp8_dequant(handle, w_ptr, stream) -> None:
+    _ok(_L().glq_fp8_dequant(handle, w_ptr, stream), "glq_fp8_dequant")
+
+
+def glq_fp8_check(handle, stream) -> None:
+    _ok(_L().glq_fp8_check(handle, stream), "glq_fp8_check")
+
+
+def glq_fp8_info(handle):
+    m, n, nb = _i64(), _i64(), ctypes.c_size_t()
+    _ok(_L().glq_fp8_info(handle, ctypes.byref(m), ctypes.byref(n), ctypes.byref(nb)), "glq_fp8_info")
+    return m.value, n.value, nb.value
+
+
 # ---------------------------------------------------------------------------
 # torch convenience (device memory and streams only)
 # ---------------------------------------------------------------------------
@@ -478,6 +529,153 @@ class GlqLinear:
     def close(self):
         if self.handle:
             glq_layer_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------------------
+# 8-bit float layers
+# ---------------------------------------------------------------------------
+
+FP8_BLOCK = 128
+
+
+def _fp8_blocks(v: int) -> int:
+    return -(-v // FP8_BLOCK)
+
+
+def _call_stream(device, stream, *tensors):
+    """The stream of a call on `device`; tensors used on a stream that is not
+    their allocator's current one are recorded there."""
+    torch = _torch()
+    current = torch.cuda.current_stream(device)
+    if stream is None or stream == current:
+        return current.cuda_stream
+    for t in tensors:
+        t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _check_input(name, t, cols, device=None):
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor [B][{'n' if cols is None else cols}]")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the layer on {device}")
+
+
+def _output(out, shape, dtype, device):
+    torch = _torch()
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.device != device or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous tensor {list(shape)} on {device}")
+    return out
+
+
+def _e4m3_matrix(name, w, device, dims=2):
+    """A CUDA e4m3 tensor with unit column stride and rows of 8-byte steps."""
+    torch = _torch()
+    if w.dim() != dims or w.dtype != torch.float8_e4m3fn:
+        raise ValueError(f"{name} must be a float8_e4m3fn tensor of {dims} dimensions")
+    w = w.to(device)
+    packed = w.stride(-1) == 1 and w.stride(-2) >= w.shape[-1] and w.stride(-2) % 8 == 0 and w.data_ptr() % 8 == 0
+    return w if packed and (dims == 2 or w.is_contiguous()) else w.contiguous().clone()
+
+
+def _block_scales(name, s, device, shape):
+    torch = _torch()
+    s = s.to(device=device, dtype=torch.float32).contiguous()
+    if tuple(s.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)} (one scale per {FP8_BLOCK} x {FP8_BLOCK} block), not {list(s.shape)}")
+    return s
+
+
+def fp8_quantize(x, q=None, s=None, stream=None):
+    """Activations x [B][n] (fp16, bf16 or fp32) rounded to e4m3 with one fp32
+    scale per token and group of 128 columns: (q [B][G * 128], s [G][B]), G =
+    ceil(n / 128), columns of q from n zero.  Several Fp8Linear layers can
+    then take them (forward_quantized).  Definition: glq_fp8_quantize."""
+    torch = _torch()
+    _check_input("x", x, None)
+    B, n = x.shape
+    G = _fp8_blocks(n)
+    q = _output(q, (B, G * FP8_BLOCK), torch.float8_e4m3fn, x.device)
+    s = _output(s, (G, B), torch.float32, x.device)
+    if q.dtype != torch.float8_e4m3fn or s.dtype != torch.float32:
+        raise ValueError("q must be float8_e4m3fn and s float32")
+    with torch.cuda.device(x.device):
+        glq_fp8_quantize(x.data_ptr(), dtype_code(x.dtype), B, n, q.data_ptr(), s.data_ptr(),
+                         _call_stream(x.device, stream, x, q, s))
+    return q, s
+
+
+class Fp8Linear:
+    """A linear layer y = x W^T with e4m3 weights W [m][n] and one fp32 scale
+    per 128 x 128 block; activations are rounded as fp8_quantize does.  The
+    weights are copied into the layer."""
+
+    def __init__(self, w, scales):
+        """w: float8_e4m3fn [m][n] (m, n multiples of 8), scales: [ceil(m/128)]
+        [ceil(n/128)].  Tensors of the CPU go to the current CUDA device.
+        Reads them on the current stream and waits for it."""
+        torch = _torch()
+        self.device = w.device if w.is_cuda else torch.device("cuda", torch.cuda.current_device())
+        w = _e4m3_matrix("w", w, self.device)
+        self.m, self.n = int(w.shape[0]), int(w.shape[1])
+        scales = _block_scales("scales", scales, self.device, (_fp8_blocks(self.m), _fp8_blocks(self.n)))
+        self.handle = 0
+        with torch.cuda.device(self.device):
+            self.handle = glq_fp8_create(self.m, self.n, w.data_ptr(), w.stride(0), scales.data_ptr(),
+                                         _call_stream(self.device, None))
+
+    def reserve(self, max_B: int):
+        glq_fp8_reserve(self.handle, max_B)
+
+    def forward(self, x, out=None, out_dtype=None, stream=None):
+        """y [B][m] of x [B][n] (fp16 or bf16) in x's dtype or out_dtype
+        (x's or float32)."""
+        _check_input("x", x, self.n, self.device)
+        out = _output(out, (x.shape[0], self.m), out_dtype or x.dtype, x.device)
+        glq_fp8_linear(self.handle, x.data_ptr(), dtype_code(x.dtype), out.data_ptr(), dtype_code(out.dtype),
+                       x.shape[0], _call_stream(self.device, stream, x, out))
+        return out
+
+    __call__ = forward
+
+    def forward_quantized(self, q, s, out=None, out_dtype=None, stream=None):
+        """y [B][m] (bfloat16 unless out or out_dtype says otherwise) of
+        activations as fp8_quantize returns them."""
+        torch = _torch()
+        G = _fp8_blocks(self.n)
+        _check_input("q", q, G * FP8_BLOCK, self.device)
+        if q.dtype != torch.float8_e4m3fn:
+            raise ValueError("q must be float8_e4m3fn")
+        B = q.shape[0]
+        if tuple(s.shape) != (G, B) or s.dtype != torch.float32 or s.device != q.device or not s.is_contiguous():
+            raise ValueError(f"s must be a contiguous float32 tensor {[G, B]} on {q.device}")
+        out = _output(out, (B, self.m), out_dtype or torch.bfloat16, q.device)
+        glq_fp8_linear_quantized(self.handle, q.data_ptr(), s.data_ptr(), out.data_ptr(), dtype_code(out.dtype), B,
+                                 _call_stream(self.device, stream, q, s, out))
+        return out
+
+    def dequant(self, stream=None):
+        """The weights as fp32 [m][n]."""
+        torch = _torch()
+        w = torch.empty((self.m, self.n), dtype=torch.float32, device=self.device)
+        glq_fp8_dequant(self.handle, w.data_ptr(), _call_stream(self.device, stream, w))
+        return w
+
+    def check(self, stream=None):
+        glq_fp8_check(self.handle, _call_stream(self.device, stream))
+
+    def close(self):
+        if self.handle:
+            glq_fp8_destroy(self.handle)
             self.handle = 0
 
     def __del__(self):

@@ -19,24 +19,12 @@
 #include "glq_internal.h"
 #include "glq_kernels.cuh"
 
+using glq::DeviceGuard;
 using glq::FoldedTable;
 
 namespace {
 
 constexpr int64_t MAX_DIM = GLQ_RHT_MAX_N;
-
-struct DeviceGuard {
-    int prev = -1;
-    bool switched = false;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) == cudaSuccess && prev != dev) {
-            switched = cudaSetDevice(dev) == cudaSuccess;
-        }
-    }
-    ~DeviceGuard() {
-        if (switched) cudaSetDevice(prev);
-    }
-};
 
 bool all_signs(const int8_t *s, int64_t k) {
     for (int64_t i = 0; i < k; ++i)
@@ -102,7 +90,7 @@ void free_layer(glq_layer L) {
 // on the GPU (one stream, or explicit ordering).
 // ---------------------------------------------------------------------------
 
-enum WsBuf { WS_XQ, WS_XH, WS_INFO, WS_PART, WS_Z, WS_PXH, WS_PINFO, WS_PZ, WS_W16, WS_COUNT };
+enum WsBuf { WS_XQ, WS_XH, WS_INFO, WS_PART, WS_Z, WS_PXH, WS_PINFO, WS_PZ, WS_W16, WS_FP8, WS_COUNT = WS_FP8 + glq::FP8_WS_COUNT };
 
 struct DeviceWs {
     void *buf[WS_COUNT] = {};
@@ -401,6 +389,15 @@ glq_status run_prefill(glq_layer L, const void *x, bool x_bf16, void *y, int y_d
 }  // namespace
 
 namespace glq {
+
+glq_status fp8_workspace(int dev, const size_t need[FP8_WS_COUNT], cudaStream_t s, void *out[FP8_WS_COUNT]) {
+    WsNeed n;
+    for (int i = 0; i < FP8_WS_COUNT; ++i) n.b[WS_FP8 + i] = need[i];
+    void *buf[WS_COUNT];
+    const glq_status st = ws_acquire(dev, n, s, buf);
+    for (int i = 0; i < FP8_WS_COUNT; ++i) out[i] = buf[WS_FP8 + i];
+    return st;
+}
 
 // fused transforms: at most this many values (tokens x largest Hadamard
 // block) are folded per task (input) or rotated by one CTA (output)

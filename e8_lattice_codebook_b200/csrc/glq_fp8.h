@@ -1,0 +1,76 @@
+// glq_fp8.h -- parameters and launchers of the 8-bit float operators: the
+// activation quantiser, the linear layer with e4m3 weights and one fp32
+// scale per 128 x 128 block, and the mixture-of-experts layer built on them.
+//
+// Device layout of a weight matrix [rows][cols] (rows on the MMA's M side):
+// tiles of 128 rows x 128 columns, 16 KB each and contiguous, tile (rt, kb)
+// at ((rt * KB) + kb) * 16 KB with KB = ceil(cols / 128).  Inside a tile a
+// row is 128 bytes and its eight 16-byte chunks are stored at chunk ^ (row &
+// 7): the 128-byte swizzle of the tensor core's K-major operand.  One bulk
+// copy of 16 KB therefore brings a ready operand tile, without a tensor map,
+// from one contiguous DRAM range.  Rows and columns past the matrix hold 0.
+// The scales are [ceil(rows / 128)][KB] fp32.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#define GLQ_FP8_BLOCK 128
+#define GLQ_FP8_TILE_BYTES 16384
+#define GLQ_FP8_MAX_DIM (1 << 20)
+
+namespace glq {
+
+// x [B][n] (dtype 0 f16, 1 bf16, 2 f32) -> q [B][KB * 128] e4m3, s [KB][B]
+struct Fp8QuantParams {
+    const void *x;
+    uint8_t *q;
+    float *s;
+    int64_t B;
+    int n, KB;
+};
+cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, cudaStream_t s, bool pdl);
+
+// rows x cols e4m3 at row distance ld (bytes, multiple of 8, src 8-byte
+// aligned) into tiles; tile row r goes to dst tile row r * rt_step + rt_off,
+// its scales likewise
+struct Fp8PackParams {
+    const uint8_t *src;
+    const float *src_scale;  // [ceil(rows/128)][KB]
+    uint8_t *dst;
+    float *dst_scale;
+    int64_t ld;
+    int rows, cols, KB;
+    int rt_step, rt_off;
+    // batch of matrices (experts): distances between two of them
+    int count;
+    int64_t src_stride, src_scale_stride, dst_tiles;
+};
+cudaError_t launch_fp8_pack(const Fp8PackParams &p, cudaStream_t s);
+
+// w [m][n] fp32 = the values the tiles and scales stand for
+cudaError_t launch_fp8_dequant(const uint8_t *tiles, const float *scale, float *w, int m, int n, int KB,
+                               cudaStream_t s);
+
+// y [B][m] = x W^T on 128-row x NT-token tiles, the K blocks of all tiles
+// dealt out evenly over the CTAs
+struct Fp8SkinnyParams {
+    const uint8_t *w;
+    const float *ws;
+    const void *x;      // source 0 / 1: f16 / bf16 [B][n], quantised on the way
+    const uint8_t *q;   // source 2: e4m3 [B][KB * 128] and
+    const float *s;     //           its scales [KB][s_ld]
+    int64_t s_ld;
+    void *y;
+    int y_dtype;
+    int m, n, B, RT, KB, TT;  // TT token tiles
+    float *part;        // [grid][2][NT][128]
+    unsigned *cnt;      // [RT * TT], zero between calls
+    unsigned *err;
+};
+int fp8_skinny_tile(int64_t B);  // NT: tokens per tile for a batch of B
+size_t fp8_skinny_part_bytes(int nt, int grid);
+cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, int source, int nt, int grid, cudaStream_t s, bool pdl);
+
+}  // namespace glq

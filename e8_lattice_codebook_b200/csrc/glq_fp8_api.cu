@@ -1,0 +1,277 @@
+// glq_fp8_api.cu -- the C ABI of the 8-bit float operators (include/glq.h):
+// argument checks, ownership of the laid-out weights, kernel choice.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <new>
+
+#include "../../include/glq.h"
+#include "glq_fp8.h"
+#include "glq_handles.h"
+
+using glq::DeviceGuard;
+
+namespace {
+
+// most tokens of one launch; a call with more runs in slices of this many
+constexpr int64_t MAX_SLICE = 8192;
+
+int64_t blocks_of(int64_t v) { return (v + GLQ_FP8_BLOCK - 1) / GLQ_FP8_BLOCK; }
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+template <typename T>
+glq_status dev_alloc(T **p, size_t bytes, size_t *total) {
+    *p = nullptr;
+    if (cudaMalloc((void **)p, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        *p = nullptr;
+        return GLQ_ERR_OOM;
+    }
+    *total += bytes;
+    return GLQ_OK;
+}
+
+glq_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return GLQ_OK;
+    cudaGetLastError();
+    return GLQ_ERR_CUDA;
+}
+
+void free_fp8(glq_fp8 L) {
+    cudaFree(L->d_w);
+    cudaFree(L->d_ws);
+    cudaFree(L->d_err);
+    cudaFree(L->d_cnt);
+    delete L;
+}
+
+// What a call of B tokens needs of the shared workspace.
+void fp8_need(glq_fp8 L, int64_t B, bool quantized, size_t need[glq::FP8_WS_COUNT]) {
+    B = std::min(B, MAX_SLICE);
+    if (B <= 0) return;
+    const int nt = glq::fp8_skinny_tile(B);
+    if (nt > 16 && !quantized) {
+        need[glq::FP8_WS_Q] = std::max(need[glq::FP8_WS_Q], (size_t)B * L->KB * GLQ_FP8_BLOCK);
+        need[glq::FP8_WS_S] = std::max(need[glq::FP8_WS_S], (size_t)B * L->KB * sizeof(float));
+    }
+    need[glq::FP8_WS_PART] = std::max(need[glq::FP8_WS_PART], glq::fp8_skinny_part_bytes(nt, L->num_sms));
+}
+
+// One slice of at most MAX_SLICE tokens: x (f16 / bf16), or q and s.
+glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, const float *s, int64_t s_ld, void *y,
+                   int y_dtype, int64_t B, cudaStream_t st) {
+    size_t need[glq::FP8_WS_COUNT] = {};
+    fp8_need(L, B, q != nullptr, need);
+    void *buf[glq::FP8_WS_COUNT];
+    const glq_status ok = glq::fp8_workspace(L->device, need, st, buf);
+    if (ok != GLQ_OK) return ok;
+    const int nt = glq::fp8_skinny_tile(B);
+    int source = 2;
+    if (!q && nt == 16) source = x_dtype;  // rounded inside the product
+    if (!q && source == 2) {
+        glq::Fp8QuantParams p{};
+        p.x = x;
+        p.q = static_cast<uint8_t *>(buf[glq::FP8_WS_Q]);
+        p.s = static_cast<float *>(buf[glq::FP8_WS_S]);
+        p.B = B;
+        p.n = (int)L->n;
+        p.KB = L->KB;
+        const glq_status e = launched(glq::launch_fp8_quantize(p, x_dtype, st, true));
+        if (e != GLQ_OK) return e;
+        q = p.q;
+        s = p.s;
+        s_ld = B;
+    }
+    glq::Fp8SkinnyParams p{};
+    p.w = L->d_w;
+    p.ws = L->d_ws;
+    p.x = x;
+    p.q = q;
+    p.s = s;
+    p.s_ld = s_ld;
+    p.y = y;
+    p.y_dtype = y_dtype;
+    p.m = (int)L->m;
+    p.n = (int)L->n;
+    p.B = (int)B;
+    p.RT = L->RT;
+    p.KB = L->KB;
+    p.TT = (int)((B + nt - 1) / nt);
+    p.part = static_cast<float *>(buf[glq::FP8_WS_PART]);
+    p.cnt = L->d_cnt;
+    p.err = L->d_err;
+    const int64_t total = (int64_t)p.RT * p.TT * p.KB;
+    const int grid = (int)std::min<int64_t>(L->num_sms, total);
+    return launched(glq::launch_fp8_skinny(p, source, nt, grid, st, true));
+}
+
+glq_status check_word(unsigned *d_err, unsigned *d_cnt, size_t cnt_bytes, cudaStream_t s) {
+    if (cudaStreamSynchronize(s) != cudaSuccess) {
+        cudaGetLastError();
+        return GLQ_ERR_CUDA;
+    }
+    unsigned err = 0;
+    if (cudaMemcpy(&err, d_err, sizeof err, cudaMemcpyDeviceToHost) != cudaSuccess) return GLQ_ERR_CUDA;
+    if (!err) return GLQ_OK;
+    // a call that gave up may have left its arrival counters half way
+    cudaMemset(d_err, 0, sizeof(unsigned));
+    cudaMemset(d_cnt, 0, cnt_bytes);
+    return (err & GLQ_DEVERR_TIMEOUT) ? GLQ_ERR_TIMEOUT : GLQ_ERR_DEVICE_CHECK;
+}
+
+bool good_dims(int64_t m, int64_t n) {
+    return m > 0 && n > 0 && !(m & 7) && !(n & 7) && m <= GLQ_FP8_MAX_DIM && n <= GLQ_FP8_MAX_DIM;
+}
+
+}  // namespace
+
+extern "C" {
+
+glq_status glq_fp8_quantize(const void *x_dev, glq_dtype x_dtype, int64_t B, int64_t n, void *q_dev, float *s_dev,
+                            void *stream) {
+    if (B < 0 || n <= 0 || (n & 7) || n > GLQ_FP8_MAX_DIM || B > 65535 * 32) return GLQ_ERR_SHAPE;
+    if (x_dtype != GLQ_F16 && x_dtype != GLQ_BF16 && x_dtype != GLQ_F32) return GLQ_ERR_DTYPE;
+    if (B == 0) return GLQ_OK;
+    if (!x_dev || !q_dev || !s_dev) return GLQ_ERR_INVALID_ARG;
+    if (!aligned(x_dev, 16) || !aligned(q_dev, 16) || !aligned(s_dev, 4)) return GLQ_ERR_INVALID_ARG;
+    glq::Fp8QuantParams p{};
+    p.x = x_dev;
+    p.q = static_cast<uint8_t *>(q_dev);
+    p.s = s_dev;
+    p.B = B;
+    p.n = (int)n;
+    p.KB = (int)blocks_of(n);
+    return launched(glq::launch_fp8_quantize(p, (int)x_dtype, static_cast<cudaStream_t>(stream), true));
+}
+
+glq_status glq_fp8_create(int64_t m, int64_t n, const void *w_dev, int64_t ldw, const float *scales_dev, void *stream,
+                          glq_fp8 *out) {
+    if (!out) return GLQ_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!good_dims(m, n) || ldw < n || (ldw & 7)) return GLQ_ERR_SHAPE;
+    if (!w_dev || !scales_dev || !aligned(w_dev, 8) || !aligned(scales_dev, 4)) return GLQ_ERR_INVALID_ARG;
+    glq_fp8 L = new (std::nothrow) glq_fp8_s;
+    if (!L) return GLQ_ERR_OOM;
+    L->m = m;
+    L->n = n;
+    L->RT = (int)blocks_of(m);
+    L->KB = (int)blocks_of(n);
+    const int64_t tiles = (int64_t)L->RT * L->KB;
+    L->cnt_bytes = (size_t)L->RT * (MAX_SLICE / 128) * sizeof(unsigned);
+    glq_status st = GLQ_OK;
+    if (cudaGetDevice(&L->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&L->num_sms, cudaDevAttrMultiProcessorCount, L->device) != cudaSuccess) {
+        cudaGetLastError();
+        st = GLQ_ERR_CUDA;
+    }
+    if (st == GLQ_OK) st = dev_alloc(&L->d_w, (size_t)tiles * GLQ_FP8_TILE_BYTES, &L->device_bytes);
+    if (st == GLQ_OK) st = dev_alloc(&L->d_ws, (size_t)tiles * sizeof(float), &L->device_bytes);
+    if (st == GLQ_OK) st = dev_alloc(&L->d_err, sizeof(unsigned), &L->device_bytes);
+    if (st == GLQ_OK) st = dev_alloc(&L->d_cnt, L->cnt_bytes, &L->device_bytes);
+    if (st == GLQ_OK) {
+        glq::Fp8PackParams p{};
+        p.src = static_cast<const uint8_t *>(w_dev);
+        p.src_scale = scales_dev;
+        p.dst = L->d_w;
+        p.dst_scale = L->d_ws;
+        p.ld = ldw;
+        p.rows = (int)m;
+        p.cols = (int)n;
+        p.KB = L->KB;
+        p.rt_step = 1;
+        p.count = 1;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if (cudaMemsetAsync(L->d_err, 0, sizeof(unsigned), s) != cudaSuccess ||
+            cudaMemsetAsync(L->d_cnt, 0, L->cnt_bytes, s) != cudaSuccess ||
+            glq::launch_fp8_pack(p, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess) {
+            cudaGetLastError();
+            st = GLQ_ERR_CUDA;
+        }
+    }
+    if (st != GLQ_OK) {
+        free_fp8(L);
+        return st;
+    }
+    *out = L;
+    return GLQ_OK;
+}
+
+glq_status glq_fp8_destroy(glq_fp8 layer) {
+    if (!layer) return GLQ_ERR_INVALID_ARG;
+    DeviceGuard guard(layer->device);
+    free_fp8(layer);
+    return GLQ_OK;
+}
+
+glq_status glq_fp8_reserve(glq_fp8 layer, int64_t max_B) {
+    if (!layer) return GLQ_ERR_INVALID_ARG;
+    if (max_B < 0) return GLQ_ERR_SHAPE;
+    DeviceGuard guard(layer->device);
+    size_t need[glq::FP8_WS_COUNT] = {};
+    for (int64_t B : {(int64_t)16, (int64_t)32, (int64_t)64, max_B}) fp8_need(layer, std::min(B, max_B), false, need);
+    void *buf[glq::FP8_WS_COUNT];
+    return glq::fp8_workspace(layer->device, need, 0, buf);
+}
+
+glq_status glq_fp8_linear(glq_fp8 L, const void *x_dev, glq_dtype x_dtype, void *y_dev, glq_dtype y_dtype, int64_t B,
+                          void *stream) {
+    if (!L) return GLQ_ERR_INVALID_ARG;
+    if (B < 0) return GLQ_ERR_SHAPE;
+    if (x_dtype != GLQ_F16 && x_dtype != GLQ_BF16) return GLQ_ERR_DTYPE;
+    if (y_dtype != x_dtype && y_dtype != GLQ_F32) return GLQ_ERR_DTYPE;
+    if (B == 0) return GLQ_OK;
+    if (!x_dev || !y_dev || !aligned(x_dev, 16) || !aligned(y_dev, 16)) return GLQ_ERR_INVALID_ARG;
+    DeviceGuard guard(L->device);
+    const size_t ye = y_dtype == GLQ_F32 ? 4 : 2;
+    for (int64_t b = 0; b < B; b += MAX_SLICE) {
+        const glq_status st = run_fp8(L, static_cast<const char *>(x_dev) + (size_t)b * L->n * 2, (int)x_dtype, nullptr,
+                                      nullptr, 0, static_cast<char *>(y_dev) + (size_t)b * L->m * ye, (int)y_dtype,
+                                      std::min(MAX_SLICE, B - b), static_cast<cudaStream_t>(stream));
+        if (st != GLQ_OK) return st;
+    }
+    return GLQ_OK;
+}
+
+glq_status glq_fp8_linear_quantized(glq_fp8 L, const void *q_dev, const float *s_dev, void *y_dev, glq_dtype y_dtype,
+                                    int64_t B, void *stream) {
+    if (!L) return GLQ_ERR_INVALID_ARG;
+    if (B < 0) return GLQ_ERR_SHAPE;
+    if (y_dtype != GLQ_F16 && y_dtype != GLQ_BF16 && y_dtype != GLQ_F32) return GLQ_ERR_DTYPE;
+    if (B == 0) return GLQ_OK;
+    if (!q_dev || !s_dev || !y_dev || !aligned(q_dev, 16) || !aligned(s_dev, 4) || !aligned(y_dev, 16))
+        return GLQ_ERR_INVALID_ARG;
+    DeviceGuard guard(L->device);
+    const size_t ye = y_dtype == GLQ_F32 ? 4 : 2;
+    for (int64_t b = 0; b < B; b += MAX_SLICE) {
+        const glq_status st =
+            run_fp8(L, nullptr, 0, static_cast<const uint8_t *>(q_dev) + (size_t)b * L->KB * GLQ_FP8_BLOCK, s_dev + b, B,
+                    static_cast<char *>(y_dev) + (size_t)b * L->m * ye, (int)y_dtype, std::min(MAX_SLICE, B - b),
+                    static_cast<cudaStream_t>(stream));
+        if (st != GLQ_OK) return st;
+    }
+    return GLQ_OK;
+}
+
+glq_status glq_fp8_dequant(glq_fp8 L, float *w_dev, void *stream) {
+    if (!L || !w_dev || !aligned(w_dev, 4)) return GLQ_ERR_INVALID_ARG;
+    DeviceGuard guard(L->device);
+    return launched(glq::launch_fp8_dequant(L->d_w, L->d_ws, w_dev, (int)L->m, (int)L->n, L->KB,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+glq_status glq_fp8_check(glq_fp8 L, void *stream) {
+    if (!L) return GLQ_ERR_INVALID_ARG;
+    DeviceGuard guard(L->device);
+    return check_word(L->d_err, L->d_cnt, L->cnt_bytes, static_cast<cudaStream_t>(stream));
+}
+
+glq_status glq_fp8_info(glq_fp8 L, int64_t *m, int64_t *n, size_t *device_bytes) {
+    if (!L) return GLQ_ERR_INVALID_ARG;
+    if (m) *m = L->m;
+    if (n) *n = L->n;
+    if (device_bytes) *device_bytes = L->device_bytes;
+    return GLQ_OK;
+}
+
+}  // extern "C"

@@ -102,7 +102,41 @@ struct glq_layer_s {
 
 inline int64_t stream_cols(glq_layer L) { return (int64_t)L->KC * GLQ_CHUNK_K; }
 
+// A linear layer with e4m3 weights and 128 x 128 block scales.
+struct glq_fp8_s {
+    int64_t m = 0, n = 0;
+    int RT = 0, KB = 0;           // 128-row tiles, 128-column blocks
+    int device = 0, num_sms = 0;
+    uint8_t *d_w = nullptr;       // [RT][KB] operand tiles (glq_fp8.h)
+    float *d_ws = nullptr;        // [RT][KB]
+    unsigned *d_err = nullptr;
+    unsigned *d_cnt = nullptr;    // output-tile arrival counters, zero between calls
+    size_t cnt_bytes = 0;
+    size_t device_bytes = 0;
+};
+
 namespace glq {
+
+// Makes `dev` the current device while it lives.
+struct DeviceGuard {
+    int prev = -1;
+    bool switched = false;
+    explicit DeviceGuard(int dev) {
+        if (cudaGetDevice(&prev) == cudaSuccess && prev != dev) {
+            switched = cudaSetDevice(dev) == cudaSuccess;
+        }
+    }
+    ~DeviceGuard() {
+        if (switched) cudaSetDevice(prev);
+    }
+};
+
+// The 8-bit float operators' buffers in the device's shared workspace:
+// rounded activations, their scales, partial sums, expert activations.
+enum Fp8Ws { FP8_WS_Q, FP8_WS_S, FP8_WS_PART, FP8_WS_H, FP8_WS_COUNT };
+// Makes each at least need[i] bytes (the rules of the shared workspace hold:
+// growth synchronises, and is refused during stream capture).
+glq_status fp8_workspace(int dev, const size_t need[FP8_WS_COUNT], cudaStream_t s, void *out[FP8_WS_COUNT]);
 
 // How one decode call of nb <= 16 tokens runs: the GEMV split plan and
 // whether the input / output transforms are fused into the GEMV launch.

@@ -76,6 +76,7 @@ typedef enum { GLQ_F16 = 0, GLQ_BF16 = 1, GLQ_F32 = 2 } glq_dtype;
 /* Opaque handles; `void*` stream arguments are cudaStream_t (0 = legacy). */
 typedef struct glq_codebook_s *glq_codebook;
 typedef struct glq_layer_s *glq_layer;
+typedef struct glq_fp8_s *glq_fp8;
 
 /* Human-readable name of a status.  Never NULL; static storage. */
 GLQ_API const char *glq_status_str(glq_status s);
@@ -464,6 +465,91 @@ GLQ_API glq_status glq_decode_plan(glq_layer layer, int64_t B, int32_t *warps, i
 /* Layer geometry, for callers sizing buffers.  Any output may be NULL. */
 GLQ_API glq_status glq_layer_info(glq_layer layer, int64_t *m, int64_t *n, int32_t *bpw,
                           size_t *device_bytes);
+
+/*
+ * ---------------------------------------------------------------------------
+ * 8-bit float layers.  A model compressed with GLQ keeps some of its linear
+ * layers in 8-bit floating point instead (layers that lose too much below 8
+ * bits, output heads, experts).  Their weights are e4m3 with one fp32 scale
+ * for each 128 x 128 block, their activations are rounded to e4m3 with one
+ * fp32 scale for each token and group of 128 columns:
+ *
+ *     y[b][r] = sum_kb s[kb][b] ws[r/128][kb] sum_{k in kb} q[b][k] w[r][k]
+ *
+ * Sums are fp32, the result is rounded once to y's dtype.  Threading,
+ * ordering, the shared workspace and errors are as for glq_linear above.
+ * (No counterpart in the GLQ pages.)
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * glq_fp8_quantize -- the activation rounding of the 8-bit float layers, for
+ * callers that share it between layers (q / k / v, gate / up).  For token b
+ * and group g of 128 columns (the last one may be short):
+ *     a = max(max |x|, 2^-110), s[g][b] = a / 448, q = e4m3(x (448 / a)),
+ * quotients and product in fp32, every rounding to nearest even.  A NaN makes
+ * its whole group NaN; an infinity gives the scale infinity and itself NaN.
+ * x_dev: device [B][n], GLQ_F16, GLQ_BF16 or GLQ_F32, 16-byte aligned.
+ * q_dev: device e4m3 [B][G * 128], G = ceil(n / 128), 16-byte aligned,
+ *   columns from n are set to 0.  s_dev: device fp32 [G][B].
+ * n a positive multiple of 8, at most 2^20; 0 <= B <= 2097120.  Runs on the
+ * current device.  Errors: GLQ_ERR_SHAPE, GLQ_ERR_DTYPE, GLQ_ERR_INVALID_ARG
+ * (null or misaligned), GLQ_ERR_CUDA.  Asynchronous.
+ */
+GLQ_API glq_status glq_fp8_quantize(const void *x_dev, glq_dtype x_dtype, int64_t B, int64_t n, void *q_dev,
+                                    float *s_dev, void *stream);
+
+/*
+ * glq_fp8_create -- build an 8-bit float linear layer on the current device.
+ * m, n: output / input features, positive multiples of 8, at most 2^20.
+ * w_dev: device e4m3 [m][n], rows ldw bytes apart (ldw >= n, a multiple of
+ *   8), 8-byte aligned; scales_dev: device fp32 [ceil(m/128)][ceil(n/128)].
+ *   Both are read on `stream` and copied (re-laid-out for the kernels); they
+ *   may be freed once the call returns.  A NaN weight or a non-finite scale
+ *   makes the outputs it reaches NaN or infinite.
+ * Errors: GLQ_ERR_INVALID_ARG, GLQ_ERR_SHAPE, GLQ_ERR_OOM, GLQ_ERR_CUDA (a
+ *   capturing stream among its causes).  Synchronises `stream`.
+ */
+GLQ_API glq_status glq_fp8_create(int64_t m, int64_t n, const void *w_dev, int64_t ldw, const float *scales_dev,
+                                  void *stream, glq_fp8 *out);
+GLQ_API glq_status glq_fp8_destroy(glq_fp8 layer);
+
+/*
+ * glq_fp8_reserve -- glq_layer_reserve for an 8-bit float layer: afterwards
+ * calls with B <= max_B allocate nothing and may be captured in a CUDA graph.
+ */
+GLQ_API glq_status glq_fp8_reserve(glq_fp8 layer, int64_t max_B);
+
+/*
+ * glq_fp8_linear -- y = x W^T with x rounded as glq_fp8_quantize does.
+ * x_dev: device [B][n] (GLQ_F16 or GLQ_BF16), y_dev: device [B][m] (x's dtype
+ * or GLQ_F32), both row-major and 16-byte aligned.  B >= 0 (0 is a no-op).
+ * Errors as glq_linear.  Asynchronous.
+ */
+GLQ_API glq_status glq_fp8_linear(glq_fp8 layer, const void *x_dev, glq_dtype x_dtype, void *y_dev,
+                                  glq_dtype y_dtype, int64_t B, void *stream);
+
+/*
+ * glq_fp8_linear_quantized -- the same from activations that are already
+ * rounded: q_dev e4m3 [B][ceil(n/128) * 128] (16-byte aligned, columns from n
+ * zero) and s_dev fp32 [ceil(n/128)][B], as glq_fp8_quantize writes them.
+ * y_dtype: any.  Errors as glq_linear.  Asynchronous.
+ */
+GLQ_API glq_status glq_fp8_linear_quantized(glq_fp8 layer, const void *q_dev, const float *s_dev, void *y_dev,
+                                            glq_dtype y_dtype, int64_t B, void *stream);
+
+/*
+ * glq_fp8_dequant -- the layer's weights as fp32 values, w_dev [m][n]
+ * row-major: each is fp32(w * scale).  Errors: GLQ_ERR_INVALID_ARG,
+ * GLQ_ERR_CUDA.  Asynchronous.
+ */
+GLQ_API glq_status glq_fp8_dequant(glq_fp8 layer, float *w_dev, void *stream);
+
+/* glq_fp8_check -- glq_layer_check for an 8-bit float layer. */
+GLQ_API glq_status glq_fp8_check(glq_fp8 layer, void *stream);
+
+/* Layer geometry.  Any output may be NULL. */
+GLQ_API glq_status glq_fp8_info(glq_fp8 layer, int64_t *m, int64_t *n, size_t *device_bytes);
 
 #ifdef __cplusplus
 }
