@@ -543,38 +543,42 @@ class GlqLinear:
 # ---------------------------------------------------------------------------
 
 FP8_BLOCK = 128
+_DTYPE_CODES = {}  # torch dtype -> code, as they are met
+
 
 
 def _fp8_blocks(v: int) -> int:
     return -(-v // FP8_BLOCK)
 
 
-def _call_stream(device, stream, *tensors):
-    """The stream of a call on `device`; tensors used on a stream that is not
-    their allocator's current one are recorded there."""
-    torch = _torch()
-    current = torch.cuda.current_stream(device)
-    if stream is None or stream == current:
-        return current.cuda_stream
+def _call_stream(index, stream, *tensors):
+    """The raw stream of a call on device `index`; tensors used on a stream
+    that is not their allocator's current one are recorded there."""
+    current = _torch()._C._cuda_getCurrentRawStream(index)
+    if stream is None or stream.cuda_stream == current:
+        return current
     for t in tensors:
         t.record_stream(stream)
     return stream.cuda_stream
 
 
-def _check_input(name, t, cols, device=None):
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or not t.is_cuda or not t.is_contiguous():
+def _dtype_code(t):
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        code = _DTYPE_CODES[t.dtype] = dtype_code(t.dtype)  # refuses what it does not know
+    return code
+
+
+def _check_input(name, t, cols, index=None):
+    if t.dim() != 2 or (cols is not None and t.size(1) != cols) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor [B][{'n' if cols is None else cols}]")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the layer on {device}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the layer on cuda:{index}")
 
 
-def _output(out, shape, dtype, device):
-    torch = _torch()
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or out.device != device or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous tensor {list(shape)} on {device}")
-    return out
+def _check_output(name, t, shape, index):
+    if tuple(t.shape) != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor {list(shape)} on cuda:{index}")
 
 
 def _e4m3_matrix(name, w, device, dims=2):
@@ -602,15 +606,24 @@ def fp8_quantize(x, q=None, s=None, stream=None):
     then take them (forward_quantized).  Definition: glq_fp8_quantize."""
     torch = _torch()
     _check_input("x", x, None)
-    B, n = x.shape
+    (B, n), index = x.shape, x.get_device()
     G = _fp8_blocks(n)
-    q = _output(q, (B, G * FP8_BLOCK), torch.float8_e4m3fn, x.device)
-    s = _output(s, (G, B), torch.float32, x.device)
+    if q is None:
+        q = torch.empty((B, G * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        _check_output("q", q, (B, G * FP8_BLOCK), index)
+    if s is None:
+        s = torch.empty((G, B), dtype=torch.float32, device=x.device)
+    else:
+        _check_output("s", s, (G, B), index)
     if q.dtype != torch.float8_e4m3fn or s.dtype != torch.float32:
         raise ValueError("q must be float8_e4m3fn and s float32")
-    with torch.cuda.device(x.device):
-        glq_fp8_quantize(x.data_ptr(), dtype_code(x.dtype), B, n, q.data_ptr(), s.data_ptr(),
-                         _call_stream(x.device, stream, x, q, s))
+    args = (x.data_ptr(), _dtype_code(x), B, n, q.data_ptr(), s.data_ptr(), _call_stream(index, stream, x, q, s))
+    if index == torch.cuda.current_device():
+        glq_fp8_quantize(*args)
+    else:
+        with torch.cuda.device(index):
+            glq_fp8_quantize(*args)
     return q, s
 
 
@@ -625,13 +638,14 @@ class Fp8Linear:
         Reads them on the current stream and waits for it."""
         torch = _torch()
         self.device = w.device if w.is_cuda else torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         w = _e4m3_matrix("w", w, self.device)
         self.m, self.n = int(w.shape[0]), int(w.shape[1])
         scales = _block_scales("scales", scales, self.device, (_fp8_blocks(self.m), _fp8_blocks(self.n)))
         self.handle = 0
         with torch.cuda.device(self.device):
             self.handle = glq_fp8_create(self.m, self.n, w.data_ptr(), w.stride(0), scales.data_ptr(),
-                                         _call_stream(self.device, None))
+                                         _call_stream(self._index, None))
 
     def reserve(self, max_B: int):
         glq_fp8_reserve(self.handle, max_B)
@@ -639,10 +653,14 @@ class Fp8Linear:
     def forward(self, x, out=None, out_dtype=None, stream=None):
         """y [B][m] of x [B][n] (fp16 or bf16) in x's dtype or out_dtype
         (x's or float32)."""
-        _check_input("x", x, self.n, self.device)
-        out = _output(out, (x.shape[0], self.m), out_dtype or x.dtype, x.device)
-        glq_fp8_linear(self.handle, x.data_ptr(), dtype_code(x.dtype), out.data_ptr(), dtype_code(out.dtype),
-                       x.shape[0], _call_stream(self.device, stream, x, out))
+        _check_input("x", x, self.n, self._index)
+        B = x.size(0)
+        if out is None:
+            out = x.new_empty((B, self.m), dtype=out_dtype)
+        else:
+            _check_output("out", out, (B, self.m), self._index)
+        glq_fp8_linear(self.handle, x.data_ptr(), _dtype_code(x), out.data_ptr(), _dtype_code(out), B,
+                       _call_stream(self._index, stream, x, out))
         return out
 
     __call__ = forward
@@ -652,26 +670,30 @@ class Fp8Linear:
         activations as fp8_quantize returns them."""
         torch = _torch()
         G = _fp8_blocks(self.n)
-        _check_input("q", q, G * FP8_BLOCK, self.device)
+        _check_input("q", q, G * FP8_BLOCK, self._index)
         if q.dtype != torch.float8_e4m3fn:
             raise ValueError("q must be float8_e4m3fn")
-        B = q.shape[0]
-        if tuple(s.shape) != (G, B) or s.dtype != torch.float32 or s.device != q.device or not s.is_contiguous():
-            raise ValueError(f"s must be a contiguous float32 tensor {[G, B]} on {q.device}")
-        out = _output(out, (B, self.m), out_dtype or torch.bfloat16, q.device)
-        glq_fp8_linear_quantized(self.handle, q.data_ptr(), s.data_ptr(), out.data_ptr(), dtype_code(out.dtype), B,
-                                 _call_stream(self.device, stream, q, s, out))
+        B = q.size(0)
+        _check_output("s", s, (G, B), self._index)
+        if s.dtype != torch.float32:
+            raise ValueError("s must be float32")
+        if out is None:
+            out = s.new_empty((B, self.m), dtype=out_dtype or torch.bfloat16)
+        else:
+            _check_output("out", out, (B, self.m), self._index)
+        glq_fp8_linear_quantized(self.handle, q.data_ptr(), s.data_ptr(), out.data_ptr(), _dtype_code(out), B,
+                                 _call_stream(self._index, stream, q, s, out))
         return out
 
     def dequant(self, stream=None):
         """The weights as fp32 [m][n]."""
         torch = _torch()
         w = torch.empty((self.m, self.n), dtype=torch.float32, device=self.device)
-        glq_fp8_dequant(self.handle, w.data_ptr(), _call_stream(self.device, stream, w))
+        glq_fp8_dequant(self.handle, w.data_ptr(), _call_stream(self._index, stream, w))
         return w
 
     def check(self, stream=None):
-        glq_fp8_check(self.handle, _call_stream(self.device, stream))
+        glq_fp8_check(self.handle, _call_stream(self._index, stream))
 
     def close(self):
         if self.handle:

@@ -128,23 +128,83 @@ __global__ void __launch_bounds__(256) fp8_dequant_kernel(const uint8_t *tiles, 
 // bytes whatever m and n are; a tile whose blocks fall to several CTAs is
 // summed from their parts, in the order of the CTAs, by the CTA that arrives
 // last.
-// SOURCE 0 / 1: f16 / bf16 activations rounded on the way; 2: e4m3 and scales.
+// SOURCE 0 / 1: f16 / bf16 activations rounded on the way; 2: e4m3 rows (by
+// TMA: 128 columns x NT tokens, 128-byte swizzle) and their scales.
 // ---------------------------------------------------------------------------
 
+// y[tok0 .. tok0 + live)[row0 .. row0 + 128) = the sum of a tile's parts, by
+// the 256 drain threads: a thread has 4 rows of one token in eight, and the
+// loads of four such tokens in flight.
+__device__ __forceinline__ void sum_parts(const Fp8SkinnyParams &p, int nt, int c0, int c1, int tok0, int live, int row0,
+                                          int dtid) {
+    const int r4 = (dtid & 31) * 4, jt = dtid >> 5;
+    const int64_t cstep = (int64_t)2 * nt * 128;
+    // the first part is its CTA's last tile (slot 1), the others their CTAs' first (slot 0)
+    const float *first = p.part + c0 * cstep + (int64_t)nt * 128 + r4, *rest = p.part + (c0 + 1) * cstep + r4;
+    for (int j0 = jt; j0 < live; j0 += 32) {
+        float4 sum[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j0 + 8 * i < live) sum[i] = __ldcg(reinterpret_cast<const float4 *>(first + (j0 + 8 * i) * 128));
+#pragma unroll 4
+        for (int c = c0 + 1; c <= c1; ++c) {
+            const float *src = rest + (c - c0 - 1) * cstep;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (j0 + 8 * i >= live) continue;
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + (j0 + 8 * i) * 128));
+                sum[i].x += v.x;
+                sum[i].y += v.y;
+                sum[i].z += v.z;
+                sum[i].w += v.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = row0 + r4;  // m is a multiple of 8: four rows are in or out together
+            if (j0 + 8 * i < live && row < p.m) store_y4(p.y, p.y_dtype, (int64_t)(tok0 + j0 + 8 * i) * p.m + row, sum[i]);
+        }
+    }
+}
+
 template <int NT, int SOURCE>
-__global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(Fp8SkinnyParams p) {
+__global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __grid_constant__ CUtensorMap qmap,
+                                                                     Fp8SkinnyParams p) {
+    constexpr bool ROUND = SOURCE != 2;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) Pipe<NT> pipe;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t total = (int64_t)p.RT * p.TT * p.KB;
-    const int G = gridDim.x, cta = blockIdx.x;
-    const int64_t b0 = range_begin(cta, total, G), b1 = range_begin(cta + 1, total, G);
-    const uint32_t nblk = (uint32_t)(b1 - b0);
+    const uint32_t KB = p.KB, TT = p.TT, total = p.RT * TT * KB, G = gridDim.x, cta = blockIdx.x;
+    const uint32_t b0 = range_begin(cta, total, G), nblk = range_begin(cta + 1, total, G) - b0;
 
-    if (tid == 0) pipe.init();
+    uint32_t it = 0;  // warp 0: blocks whose copies have been started
+    uint32_t tile = b0 / KB, kb = b0 - tile * KB, rt = tile / TT, tt = tile - rt * TT;
+    auto next_block = [&]() {
+        if (++kb == KB) {
+            kb = 0;
+            if (++tt == TT) tt = 0, ++rt;
+        }
+    };
+    auto w_tile = [&]() { return p.w + ((int64_t)rt * KB + kb) * GLQ_FP8_TILE_BYTES; };
+    if (warp == 0) {
+        pipe.init(lane);
+        __syncwarp();
+        if (lane == 0) {  // weights are constant: the first copies start at once
+            const uint32_t n = min(nblk, (uint32_t)Pipe<NT>::STAGES);
+            const uint32_t rt0 = rt, tt0 = tt, kb0 = kb;
+            for (; it < n; ++it, next_block()) pipe_load<NT, ROUND>(pipe, smem, it, w_tile(), ROUND ? 0 : NT * 128, p.err);
+            if (!ROUND) {
+                sm100::prefetch_tensormap(&qmap);
+                pdl_wait();  // the rounded tokens come from the kernel before
+                rt = rt0, tt = tt0, kb = kb0;
+                for (uint32_t i = 0; i < n; ++i, next_block())
+                    sm100::tma_load_2d(pipe_x_tile<NT>(smem, i), &qmap, &pipe.w_full[i], kb * GLQ_FP8_BLOCK, tt * NT);
+            }
+        }
+    }
     if (warp == 1) {
-        sm100::tmem_alloc(&pipe.tmem, 512);
+        sm100::tmem_alloc(&pipe.tmem, Pipe<NT>::TMEM_COLS);
         sm100::tmem_relinquish();
     }
     sm100::tc_fence_before();
@@ -153,80 +213,64 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(Fp8SkinnyPa
     pdl_launch_dependents();
 
     if (warp == 0) {
-        if (lane == 0) {  // weights are constant: no wait for the kernel before
-            uint32_t it = 0;
-            for (; it < nblk; ++it) {
-                const int64_t b = b0 + it, tile = b / p.KB;
-                const int64_t rt = tile / p.TT;
-                if (!pipe_load(pipe, smem, it, p.w + (rt * p.KB + (b - tile * p.KB)) * GLQ_FP8_TILE_BYTES, p.err))
-                    break;
+        if (lane == 0) {
+            for (; it < nblk; ++it, next_block()) {
+                if (!pipe_load<NT, ROUND>(pipe, smem, it, w_tile(), ROUND ? 0 : NT * 128, p.err)) break;
+                if (!ROUND)
+                    sm100::tma_load_2d(pipe_x_tile<NT>(smem, it), &qmap, &pipe.w_full[it % Pipe<NT>::STAGES],
+                                       kb * GLQ_FP8_BLOCK, tt * NT);
             }
-            if (pipe.abort) pipe_load_drain(pipe, it);
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            pipe_mma(pipe, smem, 0, nblk, p.err);
+            pipe_mma<NT, ROUND>(pipe, smem, 0, nblk, p.err);
             sm100::mma_commit(&pipe.mma_done);  // every MMA issued has completed
             sm100::mbar_wait(&pipe.mma_done, 0, WAIT_CYCLES);
         }
     } else if (warp < D_WARP0) {
         pdl_wait();
-        for (uint32_t it = warp - X_WARP0; it < nblk; it += X_WARPS) {
-            const int64_t b = b0 + it, tile = b / p.KB;
-            const int kb = (int)(b - tile * p.KB), rt = (int)(tile / p.TT), tok0 = (int)(tile - (int64_t)rt * p.TT) * NT;
-            const int live = min(NT, p.B - tok0);
-            if (!pipe_x_begin(pipe, it, p.err)) break;
-            uint8_t *xt = smem + (it % Pipe<NT>::STAGES) * Pipe<NT>::STAGE_BYTES + GLQ_FP8_TILE_BYTES;
-            float *sc = pipe.sc[it % Pipe<NT>::SLOTS];
-            const float ws = __ldg(p.ws + (int64_t)rt * p.KB + kb);
-            if constexpr (SOURCE == 2) {
-                const int64_t ld = (int64_t)p.KB * GLQ_FP8_BLOCK;
-                const int chunk = lane & 7;
-                const uint8_t *src = p.q + (int64_t)tok0 * ld + kb * GLQ_FP8_BLOCK + chunk * 16;
-#pragma unroll 8
-                for (int r = lane >> 3; r < live; r += 4) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(src + r * ld);
-                    *reinterpret_cast<uint4 *>(xt + sw128(r, chunk)) = v;
-                }
-                for (int r = lane; r < live; r += 32) sc[r] = p.s[(int64_t)kb * p.s_ld + tok0 + r] * ws;
-            } else {
+        for (uint32_t i = warp - X_WARP0; i < nblk && warp < X_WARP0 + Pipe<NT>::X_TURN; i += Pipe<NT>::X_TURN) {
+            const uint32_t b = b0 + i, t = b / KB, k = b - t * KB, r = t / TT;
+            const int tok0 = (int)(t - r * TT) * NT, live = min(NT, p.B - tok0);
+            const float ws = __ldg(p.ws + (int64_t)r * KB + k);
+            float *sc = pipe.sc[i % Pipe<NT>::STAGES];
+            if constexpr (ROUND) {
                 using T = typename std::conditional<SOURCE == 0, __half, __nv_bfloat16>::type;
-                const int col = kb * GLQ_FP8_BLOCK + lane * 4;
-                const bool in = col < p.n;  // n is a multiple of 8
-                const T *src = static_cast<const T *>(p.x) + (int64_t)tok0 * p.n + col;
-#pragma unroll 4
-                for (int r = 0; r < live; ++r) {
-                    uint2 w = make_uint2(0, 0);
-                    if (in) w = *reinterpret_cast<const uint2 *>(src + (int64_t)r * p.n);
-                    const float2 a = unpack2<T>(w.x), c = unpack2<T>(w.y);
-                    const float v[4] = {a.x, a.y, c.x, c.y};
-                    float s;
-                    const uint32_t q = warp_quantize(v, s);
-                    *reinterpret_cast<uint32_t *>(xt + sw128(r, lane >> 2) + (lane & 3) * 4) = q;
-                    if (lane == 0) sc[r] = s * ws;
+                const int col = k * GLQ_FP8_BLOCK + lane * 4;
+                if (!pipe_x_begin(pipe, i, p.err)) break;
+                // n is a multiple of 8: a lane's four columns are in or out together
+                warp_quantize_rows(static_cast<const T *>(p.x) + (int64_t)tok0 * p.n + col, (int64_t)p.n, col < p.n, live,
+                                   pipe_x_tile<NT>(smem, i), sc, ws, lane);
+            } else {
+                float s[(NT + 31) / 32];
+#pragma unroll
+                for (int j = 0; j < (NT + 31) / 32; ++j) {
+                    const int tok = j * 32 + lane;
+                    s[j] = tok < live ? p.s[(int64_t)k * p.s_ld + tok0 + tok] * ws : 0.f;
                 }
+                if (!pipe_x_begin(pipe, i, p.err)) break;
+#pragma unroll
+                for (int j = 0; j < (NT + 31) / 32; ++j)
+                    if (j * 32 + lane < NT) sc[j * 32 + lane] = s[j];
             }
-            pipe_x_done(pipe, it, lane);
+            pipe_x_done<NT, ROUND>(pipe, i, lane);
         }
     } else {
         pdl_wait();  // y and the workspace may still be in use by the kernel before
         constexpr int HALF = NT / 2;
-        const int dw = warp - D_WARP0, quadrant = warp & 3, set = dw >> 2;
+        const int quadrant = warp & 3, set = (warp - D_WARP0) >> 2;
         const int row_l = 32 * quadrant + lane, dtid = tid - D_WARP0 * 32;
-        int64_t tile = nblk ? b0 / p.KB : 0;
-        int kb = (int)(b0 - tile * p.KB);
         uint32_t dphase = 0;
         float acc[HALF];
 #pragma unroll
         for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
-        for (uint32_t it = 0; it < nblk; ++it) {
-            if (!pipe_drain<NT, false>(pipe, it, quadrant, set, acc, p.err)) break;
-            const bool tile_end = ++kb == p.KB;
-            if (!tile_end && it + 1 < nblk) continue;
+        for (uint32_t i = 0; i < nblk; ++i) {
+            if (!pipe_drain<NT, false>(pipe, i, quadrant, set, acc, p.err)) break;
+            const bool tile_end = ++kb == KB;
+            if (!tile_end && i + 1 < nblk) continue;
             // the end of this CTA's part of the tile
-            const int rt = (int)(tile / p.TT), tok0 = (int)(tile - (int64_t)rt * p.TT) * NT;
-            const int live = min(NT, p.B - tok0);
-            const int64_t tb = tile * p.KB;  // the tile's first block
+            const int tok0 = tt * NT, live = min(NT, p.B - tok0);
+            const uint32_t tb = tile * KB;   // the tile's first block
             const bool head = b0 > tb;       // an earlier CTA has its beginning
             if (!head && tile_end) {
                 const int row = rt * 128 + row_l;
@@ -241,37 +285,31 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(Fp8SkinnyPa
 #pragma unroll
                 for (int j = 0; j < HALF; ++j)
                     if (set * HALF + j < live) __stcg(part + (set * HALF + j) * 128 + row_l, acc[j]);
-                __threadfence();
                 if (!pipe.drain_sync(dphase, p.err)) break;
-                const int c0 = range_owner(tb, total, G), c1 = range_owner(tb + p.KB - 1, total, G);
+                const int c0 = range_owner(tb, total, G), c1 = range_owner(tb + KB - 1, total, G);
                 if (dtid == 0) {
+                    __threadfence();  // the parts of all drain threads, ordered here by the barrier
                     const bool last = atom_add_acq_rel_gpu(p.cnt + tile, 1u) == (unsigned)(c1 - c0);
                     if (last) p.cnt[tile] = 0;  // as the next call expects it
+                    __threadfence();
                     pipe.last = last;
                 }
                 if (!pipe.drain_sync(dphase, p.err)) break;
-                if (pipe.last) {
-                    __threadfence();
-                    const int r = dtid & 127, row = rt * 128 + r;
-                    for (int j = dtid >> 7; j < live; j += 2) {
-                        float sum = 0.f;
-                        for (int c = c0; c <= c1; ++c)
-                            sum += __ldcg(p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * NT * 128 + j * 128 + r);
-                        if (row < p.m) store_y(p.y, p.y_dtype, (int64_t)(tok0 + j) * p.m + row, sum);
-                    }
-                }
+                if (pipe.last) sum_parts(p, NT, c0, c1, tok0, live, rt * 128, dtid);
             }
 #pragma unroll
             for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
             ++tile;
             kb = 0;
+            if (++tt == TT) tt = 0, ++rt;
         }
     }
     sm100::tc_fence_before();
     __syncthreads();
+    if (tid == 0 && pipe.abort) pipe_load_drain(pipe, it);
     if (warp == 1) {
         sm100::tc_fence_after();
-        sm100::tmem_dealloc(pipe.tmem, 512);
+        sm100::tmem_dealloc(pipe.tmem, Pipe<NT>::TMEM_COLS);
     }
 }
 
@@ -310,7 +348,8 @@ int fp8_skinny_tile(int64_t B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 
 
 size_t fp8_skinny_part_bytes(int nt, int grid) { return (size_t)grid * 2 * nt * 128 * sizeof(float); }
 
-cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, int source, int nt, int grid, cudaStream_t s, bool pdl) {
+cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, const CUtensorMap &qmap, int source, int nt, int grid,
+                              cudaStream_t s, bool pdl) {
     const void *fn;
     size_t smem;
     int key;
@@ -327,7 +366,8 @@ cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, int source, int nt, int 
     });
     if (e != cudaSuccess) return e;
     Fp8SkinnyParams q = p;
-    void *args[] = {&q};
+    CUtensorMap map = qmap;
+    void *args[] = {&map, &q};
     return launch_ex(fn, dim3(grid), dim3(PIPE_THREADS), smem, s, pdl, args);
 }
 

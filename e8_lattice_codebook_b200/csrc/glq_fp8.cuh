@@ -64,6 +64,34 @@ __device__ __forceinline__ uint32_t warp_quantize(const float v[4], float &scale
 // with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
 
+// The same for `live` rows of x (n columns, this block's from `col`; in: the
+// lane's columns exist), written as the swizzled operand tile xt, with the
+// scales times `ws`.  Eight rows are loaded before the first is rounded: one
+// at a time, each would cost a trip to L2 (13 tokens of 14336 columns: 2600
+// cycles a block).
+template <typename T>
+__device__ __forceinline__ void warp_quantize_rows(const T *src, int64_t ld, bool in, int live, uint8_t *xt, float *sc,
+                                                   float ws, int lane) {
+    for (int r0 = 0; r0 < live; r0 += 8) {
+        uint2 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[i] = make_uint2(0, 0);
+            if (in && r0 + i < live) w[i] = __ldg(reinterpret_cast<const uint2 *>(src + (int64_t)(r0 + i) * ld));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (r0 + i >= live) break;
+            const float2 a = unpack2<T>(w[i].x), c = unpack2<T>(w[i].y);
+            const float v[4] = {a.x, a.y, c.x, c.y};
+            float s;
+            const uint32_t q = warp_quantize(v, s);
+            *reinterpret_cast<uint32_t *>(xt + sw128(r0 + i, lane >> 2) + (lane & 3) * 4) = q;
+            if (lane == 0) sc[r0 + i] = s * ws;
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // tcgen05.mma kind::f8f6f4, e4m3 x e4m3 -> fp32, K = 32 per instruction
 // ---------------------------------------------------------------------------
@@ -98,12 +126,22 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t r[8]) {
 // instructions) into its own TMEM slot of NT columns, so that the MMA never
 // waits for the sum over blocks, which the drain warps hold in registers:
 // acc[token] += d * (token scale * block scale).  Roles:
-//   warp 0       bulk copies of the 16 KB weight tiles, STAGES deep
+//   warp 0       copies: the 16 KB weight tiles and, when the tokens were
+//                rounded beforehand, their NT x 128 byte tiles
 //   warp 1       MMA issue and TMEM allocation
-//   warps 2-9    token operand: one block per warp in turn, rounded or copied
-//                into the swizzled tile, with the block's NT scales
+//   warps 2-9    one block per warp in turn: the block's NT scales, and the
+//                token tile itself when it is rounded on the way
 //   warps 10-17  drain: warp & 3 is its TMEM lane quadrant (rows), the two
 //                sets of four take half of the tokens each
+// A stage is one weight tile, its token tile, its scales and its TMEM slot;
+// four barriers carry it round:
+//   w_full the copies have landed -> MMA
+//   x_full the scales (and the tile rounded on the way) are written -> drain (MMA)
+//   done   the MMA has finished -> drain (weight copy of the next use)
+//   empty  the drain has read it -> everything of the next use
+// One commit per block and one polling lane per warp: with stages and slots
+// apart and every lane polling, the MMA thread alone took 1150 cycles a block,
+// against 700 for its share of the HBM rate.
 // ---------------------------------------------------------------------------
 
 constexpr int X_WARP0 = 2, X_WARPS = 8;
@@ -114,49 +152,66 @@ constexpr int D_THREADS = D_WARPS * 32;
 template <int NT>
 struct Pipe {
     static constexpr int STAGE_BYTES = GLQ_FP8_TILE_BYTES + NT * 128;
-    // as many stages as fit beside the static arrays: 198 KB at 16 tokens, 192 KB at 128
-    static constexpr int STAGES = NT == 16 ? 11 : NT == 32 ? 10 : NT == 64 ? 8 : 6;
-    static constexpr int SLOTS = 512 / NT;  // TMEM slots
+    // as many as shared memory holds (198 KB at 16 tokens), or as TMEM does (from 64)
+    static constexpr int STAGES = NT == 16 ? 11 : NT == 32 ? 10 : NT == 64 ? 8 : 4;
+    static constexpr int TMEM_COLS = NT == 16 ? 256 : 512;
+    static_assert(STAGES * NT <= TMEM_COLS, "a slot per stage");
     static constexpr int HALF = NT / 2;     // tokens of one drain set
+    // Token-operand warps in turn.  A warp's next block is X_TURN after its
+    // last, whose begin showed block (last - STAGES) drained; the parity of a
+    // barrier tells phases apart only one back, so X_TURN may not exceed the
+    // stages.
+    static constexpr int X_TURN = STAGES < X_WARPS ? STAGES : X_WARPS;
     static constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES;
 
-    uint64_t w_full[STAGES], x_full[STAGES], empty[STAGES];
-    uint64_t acc_full[SLOTS], acc_empty[SLOTS], sc_full[SLOTS], mma_done;
-    uint64_t drain_bar;   // the drain warps among themselves: a wait that can give up
-    alignas(16) float sc[SLOTS][NT];  // (read as float4) token scale * block scale of each slot
+    uint64_t w_full[STAGES], x_full[STAGES], done[STAGES], empty[STAGES], mma_done;
+    uint64_t drain_bar;              // the drain warps among themselves: a wait that can give up
+    alignas(16) float sc[STAGES][NT];  // (read as float4) token scale * block scale
     uint32_t tmem;
     volatile int abort;
     unsigned last;  // broadcast among the drain warps
 
-    __device__ __forceinline__ void init() {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&w_full[s], 1);
-            mbar_init(&x_full[s], 1);
-            mbar_init(&empty[s], 1);
+    // one warp
+    __device__ __forceinline__ void init(int lane) {
+        if (lane < STAGES) {
+            mbar_init(&w_full[lane], 1);
+            mbar_init(&x_full[lane], 1);
+            mbar_init(&done[lane], 1);
+            mbar_init(&empty[lane], D_WARPS);
         }
-        for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(&acc_full[s], 1);
-            mbar_init(&acc_empty[s], D_WARPS);
-            mbar_init(&sc_full[s], 1);
+        if (lane == 0) {
+            mbar_init(&mma_done, 1);
+            mbar_init(&drain_bar, D_WARPS);
+            abort = 0;
         }
-        mbar_init(&mma_done, 1);
-        mbar_init(&drain_bar, D_WARPS);
-        abort = 0;
     }
     __device__ __forceinline__ void fail(unsigned *err) {
         atomicOr(err, GLQ_DEVERR_TIMEOUT);
         abort = 1;
     }
-    // false once the wait has run out here or elsewhere in the CTA
+    // false once the wait has run out, here or elsewhere in the CTA
     __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, unsigned *err) {
-        if (abort) return false;
-        if (sm100::mbar_wait(bar, parity, WAIT_CYCLES)) return true;
-        fail(err);
-        return false;
+        if (sm100::mbar_try(bar, parity)) return true;
+        const uint64_t t0 = sm100::clock_cycles();
+        for (;;) {
+#pragma unroll 1
+            for (int i = 0; i < 64; ++i)
+                if (sm100::mbar_try(bar, parity)) return true;
+            if (abort) return false;
+            if (sm100::clock_cycles() - t0 > WAIT_CYCLES) {
+                fail(err);
+                return false;
+            }
+        }
     }
-    // the same for a whole warp: one answer, whatever each lane saw
+    // The same for a whole warp: one lane waits and __syncwarp orders the
+    // others after it.  A poll by all 32 lanes takes the mbarrier unit 32
+    // turns: every wait of the CTA then takes hundreds of cycles.
     __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, unsigned *err) {
-        return __all_sync(0xffffffffu, wait(bar, parity, err));
+        bool ok = true;
+        if ((threadIdx.x & 31) == 0) ok = wait(bar, parity, err);
+        __syncwarp();
+        return __shfl_sync(0xffffffffu, ok, 0);
     }
     // Barrier of the drain warps; phase counts the ones passed.  Not bar.sync:
     // a drain warp that gave up elsewhere would leave the others waiting.
@@ -167,75 +222,79 @@ struct Pipe {
     }
 };
 
-// Block `it` of this CTA's sequence: wait for its stage and load its tile.
-template <int NT>
-__device__ __forceinline__ bool pipe_load(Pipe<NT> &p, uint8_t *smem, uint32_t it, const uint8_t *tile, unsigned *err) {
+// The copy thread, block `it`: waits for its stage and starts its weight tile;
+// extra: bytes that other copies will bring for the block.  Where the token
+// tile is written by a warp, that warp has waited for the drain and the copy
+// may start when the MMA has finished with the tile; else the drain of the
+// TMEM slot is waited for here.
+template <int NT, bool X_WRITTEN>
+__device__ __forceinline__ bool pipe_load(Pipe<NT> &p, uint8_t *smem, uint32_t it, const uint8_t *tile, uint32_t extra,
+                                          unsigned *err) {
     const uint32_t s = it % Pipe<NT>::STAGES, use = it / Pipe<NT>::STAGES;
-    if (!p.wait(&p.empty[s], (use & 1) ^ 1, err)) return false;
-    mbar_expect_tx(&p.w_full[s], GLQ_FP8_TILE_BYTES);
+    if (!p.wait(X_WRITTEN ? &p.done[s] : &p.empty[s], (use & 1) ^ 1, err)) return false;
+    mbar_expect_tx(&p.w_full[s], GLQ_FP8_TILE_BYTES + extra);
     bulk_g2s(smem + s * Pipe<NT>::STAGE_BYTES, tile, GLQ_FP8_TILE_BYTES, &p.w_full[s]);
     return true;
 }
+template <int NT>
+__device__ __forceinline__ uint8_t *pipe_x_tile(uint8_t *smem, uint32_t it) {
+    return smem + (it % Pipe<NT>::STAGES) * Pipe<NT>::STAGE_BYTES + GLQ_FP8_TILE_BYTES;
+}
 
-// After an abort: let the copies of blocks [.., loaded) land before the CTA exits.
+// Before the CTA exits, if it gave up: let the copies of the last blocks land
+// (`loaded` blocks were issued; an earlier use of a stage has landed, or it
+// would not have been loaded again).
 template <int NT>
 __device__ __forceinline__ void pipe_load_drain(Pipe<NT> &p, uint32_t loaded) {
-    const uint32_t first = loaded > (uint32_t)Pipe<NT>::STAGES ? loaded - Pipe<NT>::STAGES : 0;
-    for (uint32_t i = first; i < loaded; ++i)
+    for (uint32_t i = loaded > (uint32_t)Pipe<NT>::STAGES ? loaded - Pipe<NT>::STAGES : 0; i < loaded; ++i)
         sm100::mbar_wait(&p.w_full[i % Pipe<NT>::STAGES], (i / Pipe<NT>::STAGES) & 1, WAIT_CYCLES);
 }
 
-// The MMA warp's one thread: blocks [it, it + count).
-template <int NT>
+// The MMA warp's one thread: blocks [it, it + count).  X_WRITTEN: the token
+// tile is written by a warp rather than copied.
+template <int NT, bool X_WRITTEN>
 __device__ __forceinline__ bool pipe_mma(Pipe<NT> &p, uint8_t *smem, uint32_t it, uint32_t count, unsigned *err) {
     const uint32_t idesc = idesc_e4m3_f32(128, NT);
-    for (const uint32_t end = it + count; it != end; ++it) {
-        const uint32_t s = it % Pipe<NT>::STAGES, use = it / Pipe<NT>::STAGES;
-        const uint32_t slot = it % Pipe<NT>::SLOTS, suse = it / Pipe<NT>::SLOTS;
-        if (!p.wait(&p.acc_empty[slot], (suse & 1) ^ 1, err) || !p.wait(&p.x_full[s], use & 1, err) ||
-            !p.wait(&p.w_full[s], use & 1, err))
-            return false;
+    const uint32_t tmem = p.tmem;
+    uint32_t s = it % Pipe<NT>::STAGES, par = (it / Pipe<NT>::STAGES) & 1;
+    for (uint32_t i = 0; i < count; ++i) {
+        if ((X_WRITTEN && !p.wait(&p.x_full[s], par, err)) || !p.wait(&p.w_full[s], par, err)) return false;
         sm100::tc_fence_after();
         uint8_t *st = smem + s * Pipe<NT>::STAGE_BYTES;
         const uint64_t a = sm100::smem_desc_sw128(st), b = sm100::smem_desc_sw128(st + GLQ_FP8_TILE_BYTES);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_f8_ss(p.tmem + slot * NT, a + 2 * kk, b + 2 * kk, idesc, kk);
-        sm100::mma_commit(&p.acc_full[slot]);
-        sm100::mma_commit(&p.empty[s]);
+        for (int kk = 0; kk < 4; ++kk) mma_f8_ss(tmem + s * NT, a + 2 * kk, b + 2 * kk, idesc, kk);
+        sm100::mma_commit(&p.done[s]);
+        if (++s == Pipe<NT>::STAGES) s = 0, par ^= 1;
     }
     return true;
 }
 
-// A token-operand warp before it writes block `it`: its stage and scale slot
-// are free.  After the writes: pipe_x_done.
+// A scale / token warp before it writes block `it`: its stage has been
+// drained.  After the writes: pipe_x_done.
 template <int NT>
 __device__ __forceinline__ bool pipe_x_begin(Pipe<NT> &p, uint32_t it, unsigned *err) {
-    const uint32_t s = it % Pipe<NT>::STAGES, slot = it % Pipe<NT>::SLOTS;
-    return p.wait_warp(&p.empty[s], ((it / Pipe<NT>::STAGES) & 1) ^ 1, err) &&
-           p.wait_warp(&p.acc_empty[slot], ((it / Pipe<NT>::SLOTS) & 1) ^ 1, err);
+    return p.wait_warp(&p.empty[it % Pipe<NT>::STAGES], ((it / Pipe<NT>::STAGES) & 1) ^ 1, err);
 }
-template <int NT>
+template <int NT, bool X_WRITTEN>
 __device__ __forceinline__ void pipe_x_done(Pipe<NT> &p, uint32_t it, int lane) {
-    sm100::fence_proxy_async_smem();  // the MMA reads the tile through the async proxy
+    if (X_WRITTEN) sm100::fence_proxy_async_smem();  // the MMA reads the tile through the async proxy
     __syncwarp();
-    if (lane == 0) {
-        sm100::mbar_arrive(&p.sc_full[it % Pipe<NT>::SLOTS]);
-        sm100::mbar_arrive(&p.x_full[it % Pipe<NT>::STAGES]);
-    }
+    if (lane == 0) sm100::mbar_arrive(&p.x_full[it % Pipe<NT>::STAGES]);
 }
 
-// A drain warp: adds block `it` to acc (its half of the tokens).  skip_zero:
+// A drain warp: adds block `it` to acc (its half of the tokens).  SKIP_ZERO:
 // tokens whose scale is 0 take no part (their operand rows are not written).
 template <int NT, bool SKIP_ZERO>
 __device__ __forceinline__ bool pipe_drain(Pipe<NT> &p, uint32_t it, int quadrant, int set, float (&acc)[NT / 2],
                                            unsigned *err) {
     constexpr int HALF = NT / 2;
     constexpr int STEP = HALF < 16 ? 8 : 16;
-    const uint32_t slot = it % Pipe<NT>::SLOTS, par = (it / Pipe<NT>::SLOTS) & 1;
-    if (!p.wait_warp(&p.sc_full[slot], par, err) || !p.wait_warp(&p.acc_full[slot], par, err)) return false;
+    const uint32_t s = it % Pipe<NT>::STAGES, par = (it / Pipe<NT>::STAGES) & 1;
+    if (!p.wait_warp(&p.done[s], par, err) || !p.wait_warp(&p.x_full[s], par, err)) return false;
     sm100::tc_fence_after();
-    const uint32_t t0 = p.tmem + ((uint32_t)(32 * quadrant) << 16) + slot * NT + set * HALF;
-    const float4 *sc = reinterpret_cast<const float4 *>(&p.sc[slot][set * HALF]);
+    const uint32_t t0 = p.tmem + ((uint32_t)(32 * quadrant) << 16) + s * NT + set * HALF;
+    const float4 *sc = reinterpret_cast<const float4 *>(&p.sc[s][set * HALF]);
 #pragma unroll
     for (int c = 0; c < HALF; c += STEP) {
         uint32_t d[STEP];
@@ -254,21 +313,41 @@ __device__ __forceinline__ bool pipe_drain(Pipe<NT> &p, uint32_t it, int quadran
     }
     sm100::tc_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&p.acc_empty[slot]);
+    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&p.empty[s]);
     return true;
 }
 
 // Blocks dealt out evenly: CTA c of G owns [c total / G, (c + 1) total / G).
-__device__ __forceinline__ int64_t range_begin(int64_t c, int64_t total, int64_t G) { return c * total / G; }
+// (total < 2^31: the blocks of 2^31 would fill more than the device's memory)
+__device__ __forceinline__ uint32_t range_begin(uint32_t c, uint32_t total, uint32_t G) {
+    return (uint32_t)((uint64_t)c * total / G);
+}
 // the CTA that owns block b
-__device__ __forceinline__ int range_owner(int64_t b, int64_t total, int64_t G) {
-    return (int)(((b + 1) * G - 1) / total);
+__device__ __forceinline__ int range_owner(uint32_t b, uint32_t total, uint32_t G) {
+    return (int)((((uint64_t)b + 1) * G - 1) / total);
 }
 
 __device__ __forceinline__ void store_y(void *y, int dtype, int64_t i, float v) {
     if (dtype == 1) static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
     else if (dtype == 0) static_cast<__half *>(y)[i] = __float2half_rn(v);
     else static_cast<float *>(y)[i] = v;
+}
+
+// four consecutive outputs, i a multiple of 4
+__device__ __forceinline__ void store_y4(void *y, int dtype, int64_t i, float4 v) {
+    if (dtype == 2) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(y) + i) = v;
+        return;
+    }
+    uint2 w;
+    if (dtype == 1) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else {
+        const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+        w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(y) + i) = w;
 }
 
 }  // namespace fp8

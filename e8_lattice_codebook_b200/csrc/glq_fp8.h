@@ -71,6 +71,8 @@ struct Fp8SkinnyParams {
 };
 int fp8_skinny_tile(int64_t B);  // NT: tokens per tile for a batch of B
 size_t fp8_skinny_part_bytes(int nt, int grid);
-cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, int source, int nt, int grid, cudaStream_t s, bool pdl);
+// qmap: source 2 only, boxes of 128 columns x nt tokens of q, 128-byte swizzle
+cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, const CUtensorMap &qmap, int source, int nt, int grid,
+                              cudaStream_t s, bool pdl);
 
 }  // namespace glq

@@ -1,5 +1,7 @@
 // glq_fp8_api.cu -- the C ABI of the 8-bit float operators (include/glq.h):
 // argument checks, ownership of the laid-out weights, kernel choice.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -38,6 +40,29 @@ glq_status launched(cudaError_t e) {
     return GLQ_ERR_CUDA;
 }
 
+// TMA descriptor of e4m3 rows [rows][cols]: boxes of 128 columns x box_rows,
+// 128-byte swizzle, zero fill past the last row.
+bool encode_rows(CUtensorMap *map, const uint8_t *q, int64_t cols, int64_t rows, int box_rows) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        cudaDriverEntryPointQueryResult r;
+        void *fn = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            fn = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols};
+    const cuuint32_t box[2] = {GLQ_FP8_BLOCK, (cuuint32_t)box_rows};
+    const cuuint32_t step[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(q), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 void free_fp8(glq_fp8 L) {
     cudaFree(L->d_w);
     cudaFree(L->d_ws);
@@ -46,12 +71,16 @@ void free_fp8(glq_fp8 L) {
     delete L;
 }
 
+// Batches whose activations the product itself rounds; above, a kernel of
+// their own rounds them first.
+bool rounds_inside(int64_t B) { return B <= 4; }
+
 // What a call of B tokens needs of the shared workspace.
 void fp8_need(glq_fp8 L, int64_t B, bool quantized, size_t need[glq::FP8_WS_COUNT]) {
     B = std::min(B, MAX_SLICE);
     if (B <= 0) return;
     const int nt = glq::fp8_skinny_tile(B);
-    if (nt > 16 && !quantized) {
+    if (!quantized && !rounds_inside(B)) {
         need[glq::FP8_WS_Q] = std::max(need[glq::FP8_WS_Q], (size_t)B * L->KB * GLQ_FP8_BLOCK);
         need[glq::FP8_WS_S] = std::max(need[glq::FP8_WS_S], (size_t)B * L->KB * sizeof(float));
     }
@@ -68,7 +97,7 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
     if (ok != GLQ_OK) return ok;
     const int nt = glq::fp8_skinny_tile(B);
     int source = 2;
-    if (!q && nt == 16) source = x_dtype;  // rounded inside the product
+    if (!q && rounds_inside(B)) source = x_dtype;
     if (!q && source == 2) {
         glq::Fp8QuantParams p{};
         p.x = x;
@@ -103,7 +132,9 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
     p.err = L->d_err;
     const int64_t total = (int64_t)p.RT * p.TT * p.KB;
     const int grid = (int)std::min<int64_t>(L->num_sms, total);
-    return launched(glq::launch_fp8_skinny(p, source, nt, grid, st, true));
+    CUtensorMap qmap{};
+    if (source == 2 && !encode_rows(&qmap, q, (int64_t)L->KB * GLQ_FP8_BLOCK, B, nt)) return GLQ_ERR_CUDA;
+    return launched(glq::launch_fp8_skinny(p, qmap, source, nt, grid, st, true));
 }
 
 glq_status check_word(unsigned *d_err, unsigned *d_cnt, size_t cnt_bytes, cudaStream_t s) {
