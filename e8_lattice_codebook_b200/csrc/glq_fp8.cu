@@ -122,103 +122,72 @@ __global__ void __launch_bounds__(256) fp8_dequant_kernel(const uint8_t *tiles, 
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens.  Reads every weight once: bound by HBM for small batches.  The
-// 128 x 128 blocks of all output tiles form one sequence, dealt out evenly
-// over the CTAs (one per SM), so that every SM streams the same number of
-// bytes whatever m and n are; a tile whose blocks fall to several CTAs is
-// summed from their parts, in the order of the CTAs, by the CTA that arrives
-// last.
+// Few tokens.  Reads every weight once: bound by HBM for small batches.  An
+// output tile is 128 weight rows x NT tokens; a cluster of C CTAs (one per SM)
+// takes tile after tile, each CTA 1 / C of its K blocks, so that few tiles
+// still keep most SMs loading.  The parts meet in distributed shared memory:
+// token j is summed by CTA j mod C of the cluster, in the order of the CTAs.
+// (Parts through global memory, summed by the CTA that arrives last, cost 3.5
+// to 5 us at the end of every call: store, atomic and load each make the trip
+// to L2.)
 // SOURCE 0 / 1: f16 / bf16 activations rounded on the way; 2: e4m3 rows (by
 // TMA: 128 columns x NT tokens, 128-byte swizzle) and their scales.
 // ---------------------------------------------------------------------------
-
-// y[tok0 .. tok0 + live)[row0 .. row0 + 128) = the sum of a tile's parts, by
-// the 256 drain threads: a thread has 4 rows of one token in eight, and the
-// loads of four such tokens in flight.
-__device__ __forceinline__ void sum_parts(const Fp8SkinnyParams &p, int nt, int c0, int c1, int tok0, int live, int row0,
-                                          int dtid) {
-    const int r4 = (dtid & 31) * 4, jt = dtid >> 5;
-    const int64_t cstep = (int64_t)2 * nt * 128;
-    // the first part is its CTA's last tile (slot 1), the others their CTAs' first (slot 0)
-    const float *first = p.part + c0 * cstep + (int64_t)nt * 128 + r4, *rest = p.part + (c0 + 1) * cstep + r4;
-    for (int j0 = jt; j0 < live; j0 += 32) {
-        float4 sum[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (j0 + 8 * i < live) sum[i] = __ldcg(reinterpret_cast<const float4 *>(first + (j0 + 8 * i) * 128));
-#pragma unroll 4
-        for (int c = c0 + 1; c <= c1; ++c) {
-            const float *src = rest + (c - c0 - 1) * cstep;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (j0 + 8 * i >= live) continue;
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + (j0 + 8 * i) * 128));
-                sum[i].x += v.x;
-                sum[i].y += v.y;
-                sum[i].z += v.z;
-                sum[i].w += v.w;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = row0 + r4;  // m is a multiple of 8: four rows are in or out together
-            if (j0 + 8 * i < live && row < p.m) store_y4(p.y, p.y_dtype, (int64_t)(tok0 + j0 + 8 * i) * p.m + row, sum[i]);
-        }
-    }
-}
 
 template <int NT, int SOURCE>
 __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __grid_constant__ CUtensorMap qmap,
                                                                      Fp8SkinnyParams p) {
     constexpr bool ROUND = SOURCE != 2;
+    constexpr int HALF = NT / 2, STAGES = Pipe<NT>::STAGES;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) Pipe<NT> pipe;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t KB = p.KB, TT = p.TT, total = p.RT * TT * KB, G = gridDim.x, cta = blockIdx.x;
-    const uint32_t b0 = range_begin(cta, total, G), nblk = range_begin(cta + 1, total, G) - b0;
+    const uint32_t C = p.C, rank = C > 1 ? sm100::cluster_ctarank() : 0;
+    const uint32_t NC = gridDim.x / C, TT = p.TT, tiles = p.RT * TT;
+    // this CTA's K blocks of every tile
+    const uint32_t k0 = rank * p.KB / C, nk = (rank + 1) * p.KB / C - k0;
+    const uint32_t first = blockIdx.x / C;
+    const uint32_t nblk = first < tiles ? ((tiles - first - 1) / NC + 1) * nk : 0;
 
-    uint32_t it = 0;  // warp 0: blocks whose copies have been started
-    uint32_t tile = b0 / KB, kb = b0 - tile * KB, rt = tile / TT, tt = tile - rt * TT;
-    auto next_block = [&]() {
-        if (++kb == KB) {
-            kb = 0;
-            if (++tt == TT) tt = 0, ++rt;
-        }
-    };
-    auto w_tile = [&]() { return p.w + ((int64_t)rt * KB + kb) * GLQ_FP8_TILE_BYTES; };
-    if (warp == 0) {
-        pipe.init(lane);
-        __syncwarp();
-        if (lane == 0) {  // weights are constant: the first copies start at once
-            const uint32_t n = min(nblk, (uint32_t)Pipe<NT>::STAGES);
-            const uint32_t rt0 = rt, tt0 = tt, kb0 = kb;
-            for (; it < n; ++it, next_block()) pipe_load<NT, ROUND>(pipe, smem, it, w_tile(), ROUND ? 0 : NT * 128, p.err);
-            if (!ROUND) {
-                sm100::prefetch_tensormap(&qmap);
-                pdl_wait();  // the rounded tokens come from the kernel before
-                rt = rt0, tt = tt0, kb = kb0;
-                for (uint32_t i = 0; i < n; ++i, next_block())
-                    sm100::tma_load_2d(pipe_x_tile<NT>(smem, i), &qmap, &pipe.w_full[i], kb * GLQ_FP8_BLOCK, tt * NT);
-            }
-        }
-    }
+    if (warp == 0) pipe.init(lane, C);
     if (warp == 1) {
         sm100::tmem_alloc(&pipe.tmem, Pipe<NT>::TMEM_COLS);
         sm100::tmem_relinquish();
     }
     sm100::tc_fence_before();
     __syncthreads();
+    if (C > 1) sm100::cluster_sync_all();  // barriers are set up before another CTA arrives on them
     sm100::tc_fence_after();
     pdl_launch_dependents();
 
+    uint32_t it = 0;  // warp 0: blocks whose copies have been started
     if (warp == 0) {
         if (lane == 0) {
-            for (; it < nblk; ++it, next_block()) {
-                if (!pipe_load<NT, ROUND>(pipe, smem, it, w_tile(), ROUND ? 0 : NT * 128, p.err)) break;
-                if (!ROUND)
-                    sm100::tma_load_2d(pipe_x_tile<NT>(smem, it), &qmap, &pipe.w_full[it % Pipe<NT>::STAGES],
-                                       kb * GLQ_FP8_BLOCK, tt * NT);
+            uint32_t t = first, k = 0, xt = first, xk = 0;
+            auto load_w = [&]() {
+                const uint8_t *w = p.w + ((int64_t)(t / TT) * p.KB + k0 + k) * GLQ_FP8_TILE_BYTES;
+                if (!pipe_load<NT, ROUND>(pipe, smem, it, w, ROUND ? 0 : NT * 128, p.err)) return false;
+                if (++k == nk) k = 0, t += NC;
+                return true;
+            };
+            auto load_x = [&](uint32_t i) {
+                sm100::tma_load_2d(pipe_x_tile<NT>(smem, i), &qmap, &pipe.w_full[i % STAGES],
+                                   (int)(k0 + xk) * GLQ_FP8_BLOCK, (int)(xt % TT) * NT);
+                if (++xk == nk) xk = 0, xt += NC;
+            };
+            if (!ROUND) sm100::prefetch_tensormap(&qmap);
+            // weights are constant: the first copies do not wait for the kernel
+            // before, which the rounded tokens come from
+            const uint32_t n = min(nblk, (uint32_t)STAGES);
+            for (; it < n; ++it) load_w();
+            if (!ROUND) {
+                pdl_wait();
+                for (uint32_t i = 0; i < n; ++i) load_x(i);
+            }
+            for (; it < nblk; ++it) {
+                if (!load_w()) break;
+                if (!ROUND) load_x(it);
             }
         }
     } else if (warp == 1) {
@@ -230,10 +199,10 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
     } else if (warp < D_WARP0) {
         pdl_wait();
         for (uint32_t i = warp - X_WARP0; i < nblk && warp < X_WARP0 + Pipe<NT>::X_TURN; i += Pipe<NT>::X_TURN) {
-            const uint32_t b = b0 + i, t = b / KB, k = b - t * KB, r = t / TT;
-            const int tok0 = (int)(t - r * TT) * NT, live = min(NT, p.B - tok0);
-            const float ws = __ldg(p.ws + (int64_t)r * KB + k);
-            float *sc = pipe.sc[i % Pipe<NT>::STAGES];
+            const uint32_t q = i / nk, t = first + q * NC, k = k0 + (i - q * nk), rt = t / TT;
+            const int tok0 = (int)(t - rt * TT) * NT, live = min(NT, p.B - tok0);
+            const float ws = __ldg(p.ws + (int64_t)rt * p.KB + k);
+            float *sc = pipe.sc[i % STAGES];
             if constexpr (ROUND) {
                 using T = typename std::conditional<SOURCE == 0, __half, __nv_bfloat16>::type;
                 const int col = k * GLQ_FP8_BLOCK + lane * 4;
@@ -256,23 +225,22 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
             pipe_x_done<NT, ROUND>(pipe, i, lane);
         }
     } else {
-        pdl_wait();  // y and the workspace may still be in use by the kernel before
-        constexpr int HALF = NT / 2;
+        pdl_wait();  // y may still be in use by the kernel before
         const int quadrant = warp & 3, set = (warp - D_WARP0) >> 2;
         const int row_l = 32 * quadrant + lane, dtid = tid - D_WARP0 * 32;
-        uint32_t dphase = 0;
+        float *red = reinterpret_cast<float *>(smem + STAGES * Pipe<NT>::STAGE_BYTES);
+        const int per = (NT + C - 1) / C;  // most tokens one CTA sums
         float acc[HALF];
+        uint32_t i = 0, round = 0;
+        for (uint32_t t = first; t < tiles; t += NC, ++round) {
+            const int rt = (int)(t / TT), tok0 = (int)(t - rt * TT) * NT, live = min(NT, p.B - tok0);
 #pragma unroll
-        for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
-        for (uint32_t i = 0; i < nblk; ++i) {
-            if (!pipe_drain<NT, false>(pipe, i, quadrant, set, acc, p.err)) break;
-            const bool tile_end = ++kb == KB;
-            if (!tile_end && i + 1 < nblk) continue;
-            // the end of this CTA's part of the tile
-            const int tok0 = tt * NT, live = min(NT, p.B - tok0);
-            const uint32_t tb = tile * KB;   // the tile's first block
-            const bool head = b0 > tb;       // an earlier CTA has its beginning
-            if (!head && tile_end) {
+            for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
+            bool ok = true;
+            for (uint32_t k = 0; k < nk && ok; ++k, ++i)
+                ok = pipe_drain<NT, false>(pipe, i, quadrant, set, acc, p.err);
+            if (!ok) break;
+            if (C == 1) {
                 const int row = rt * 128 + row_l;
                 if (row < p.m) {
 #pragma unroll
@@ -280,37 +248,42 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
                         if (set * HALF + j < live)
                             store_y(p.y, p.y_dtype, (int64_t)(tok0 + set * HALF + j) * p.m + row, acc[j]);
                 }
-            } else {
-                float *part = p.part + ((int64_t)cta * 2 + (head ? 0 : 1)) * NT * 128;
-#pragma unroll
-                for (int j = 0; j < HALF; ++j)
-                    if (set * HALF + j < live) __stcg(part + (set * HALF + j) * 128 + row_l, acc[j]);
-                if (!pipe.drain_sync(dphase, p.err)) break;
-                const int c0 = range_owner(tb, total, G), c1 = range_owner(tb + KB - 1, total, G);
-                if (dtid == 0) {
-                    __threadfence();  // the parts of all drain threads, ordered here by the barrier
-                    const bool last = atom_add_acq_rel_gpu(p.cnt + tile, 1u) == (unsigned)(c1 - c0);
-                    if (last) p.cnt[tile] = 0;  // as the next call expects it
-                    __threadfence();
-                    pipe.last = last;
-                }
-                if (!pipe.drain_sync(dphase, p.err)) break;
-                if (pipe.last) sum_parts(p, NT, c0, c1, tok0, live, rt * 128, dtid);
+                continue;
             }
+            // parts to the CTAs that sum them
+            if (!pipe.wait_warp_cluster(&pipe.red_empty, (round & 1) ^ 1, p.err)) break;
 #pragma unroll
-            for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
-            ++tile;
-            kb = 0;
-            if (++tt == TT) tt = 0, ++rt;
+            for (int j = 0; j < HALF; ++j) {
+                const int tok = set * HALF + j, own = tok / C;
+                if (tok < live) st_remote(remote_smem(red + ((int)rank * per + own) * 128 + row_l, tok - own * C), acc[j]);
+            }
+            __syncwarp();
+            if (lane < C) sm100::mbar_arrive_remote(&pipe.red_full, lane);
+            if (!pipe.wait_warp_cluster(&pipe.red_full, round & 1, p.err)) break;
+            // a warp sums one token in eight, a lane four rows
+            const int row = rt * 128 + lane * 4;
+            for (int own = dtid >> 5; own * (int)C + (int)rank < live; own += D_WARPS) {
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (uint32_t c = 0; c < C; ++c) {
+                    const float4 v = *reinterpret_cast<const float4 *>(red + ((int)c * per + own) * 128 + lane * 4);
+                    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                }
+                // m is a multiple of 8: four rows are in or out together
+                if (row < p.m) store_y4(p.y, p.y_dtype, (int64_t)(tok0 + own * (int)C + (int)rank) * p.m + row, sum);
+            }
+            __syncwarp();
+            if (lane < C) sm100::mbar_arrive_remote(&pipe.red_empty, lane);
         }
     }
     sm100::tc_fence_before();
     __syncthreads();
     if (tid == 0 && pipe.abort) pipe_load_drain(pipe, it);
+    __syncwarp();
     if (warp == 1) {
         sm100::tc_fence_after();
         sm100::tmem_dealloc(pipe.tmem, Pipe<NT>::TMEM_COLS);
     }
+    if (C > 1) sm100::cluster_sync_all();  // no CTA leaves while another may still write to it
 }
 
 template <int NT>
@@ -346,29 +319,87 @@ cudaError_t launch_fp8_dequant(const uint8_t *tiles, const float *scale, float *
 
 int fp8_skinny_tile(int64_t B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : 128; }
 
-size_t fp8_skinny_part_bytes(int nt, int grid) { return (size_t)grid * 2 * nt * 128 * sizeof(float); }
+namespace {
 
-cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, const CUtensorMap &qmap, int source, int nt, int grid,
-                              cudaStream_t s, bool pdl) {
+struct SkinnyKernel {
     const void *fn;
     size_t smem;
     int key;
+};
+
+SkinnyKernel skinny_kernel(int source, int nt) {
     switch (nt) {
-        case 16: fn = skinny_fn<16>(source), smem = Pipe<16>::SMEM_BYTES, key = 0; break;
-        case 32: fn = skinny_fn<32>(source), smem = Pipe<32>::SMEM_BYTES, key = 1; break;
-        case 64: fn = skinny_fn<64>(source), smem = Pipe<64>::SMEM_BYTES, key = 2; break;
-        case 128: fn = skinny_fn<128>(source), smem = Pipe<128>::SMEM_BYTES, key = 3; break;
-        default: return cudaErrorInvalidValue;
+        case 16: return {skinny_fn<16>(source), Pipe<16>::SMEM_BYTES, source};
+        case 32: return {skinny_fn<32>(source), Pipe<32>::SMEM_BYTES, 3 + source};
+        case 64: return {skinny_fn<64>(source), Pipe<64>::SMEM_BYTES, 6 + source};
+        default: return {skinny_fn<128>(source), Pipe<128>::SMEM_BYTES, 9 + source};
     }
+}
+
+// Sets the kernel's shared memory limit once per device.
+cudaError_t prepare(const SkinnyKernel &k) {
     static std::atomic<uint64_t> configured[12];
-    const cudaError_t e = once_per_device(configured[key * 3 + source], [fn, smem] {
-        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return once_per_device(configured[k.key], [&k] {
+        return cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
     });
+}
+
+}  // namespace
+
+cudaError_t fp8_skinny_clusters(int num_sms, int count[9]) {
+    // the clusters that fit depend on the device's layout of SMs and on one
+    // CTA per SM, not on which variant runs
+    const SkinnyKernel k = skinny_kernel(2, 16);
+    cudaError_t e = prepare(k);
+    count[0] = 0;
+    count[1] = num_sms;
+    for (int c = 2; c <= 8 && e == cudaSuccess; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(c);
+        cfg.blockDim = dim3(PIPE_THREADS);
+        cfg.dynamicSmemBytes = k.smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = c;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&count[c], k.fn, &cfg);
+    }
+    return e;
+}
+
+Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, const int clusters[9]) {
+    // One CTA takes a block in about 0.22 us by itself, all together at the
+    // HBM's rate (16 KB at 5.9 TB/s: 0.0028 us); summing the parts of a split
+    // tile costs about as much as four blocks.
+    Fp8SkinnyPlan best{1, (int)(tiles < clusters[1] ? tiles : clusters[1])};
+    double best_t = 1e30;
+    for (int c = 1; c <= 8 && c <= KB; ++c) {
+        if (clusters[c] < 1) continue;
+        const int64_t nc = tiles < clusters[c] ? tiles : clusters[c];
+        const int64_t rounds = (tiles + nc - 1) / nc;
+        const double alone = rounds * ((KB + c - 1) / c) * 0.22;
+        const double hbm = (double)tiles * KB * 0.0028;
+        const double t = (alone > hbm ? alone : hbm) + (c > 1 ? 0.9 : 0.0);
+        if (t < best_t * 0.98) {
+            best_t = t;
+            best = {c, (int)nc};
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, const CUtensorMap &qmap, int source, int nt, int clusters,
+                              cudaStream_t s, bool pdl) {
+    const SkinnyKernel k = skinny_kernel(source, nt);
+    const cudaError_t e = prepare(k);
     if (e != cudaSuccess) return e;
     Fp8SkinnyParams q = p;
     CUtensorMap map = qmap;
     void *args[] = {&map, &q};
-    return launch_ex(fn, dim3(grid), dim3(PIPE_THREADS), smem, s, pdl, args);
+    return launch_ex(k.fn, dim3(clusters * p.C), dim3(PIPE_THREADS), k.smem, s, pdl, args, p.C);
 }
 
 }  // namespace glq

@@ -152,8 +152,8 @@ constexpr int D_THREADS = D_WARPS * 32;
 template <int NT>
 struct Pipe {
     static constexpr int STAGE_BYTES = GLQ_FP8_TILE_BYTES + NT * 128;
-    // as many as shared memory holds (198 KB at 16 tokens), or as TMEM does (from 64)
-    static constexpr int STAGES = NT == 16 ? 11 : NT == 32 ? 10 : NT == 64 ? 8 : 4;
+    // as many as shared memory holds beside the parts buffer, or as TMEM does (128 tokens)
+    static constexpr int STAGES = NT == 16 ? 11 : NT == 32 ? 9 : NT == 64 ? 7 : 4;
     static constexpr int TMEM_COLS = NT == 16 ? 256 : 512;
     static_assert(STAGES * NT <= TMEM_COLS, "a slot per stage");
     static constexpr int HALF = NT / 2;     // tokens of one drain set
@@ -162,17 +162,22 @@ struct Pipe {
     // barrier tells phases apart only one back, so X_TURN may not exceed the
     // stages.
     static constexpr int X_TURN = STAGES < X_WARPS ? STAGES : X_WARPS;
-    static constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES;
+    // parts of the tokens a CTA sums: at most NT / C + 1 tokens from each of C <= 8 CTAs
+    static constexpr int RED_BYTES = (NT + 8) * 128 * 4;
+    static constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + RED_BYTES;
+    static_assert(SMEM_BYTES + 4096 <= 227 * 1024, "shared memory");
 
     uint64_t w_full[STAGES], x_full[STAGES], done[STAGES], empty[STAGES], mma_done;
-    uint64_t drain_bar;              // the drain warps among themselves: a wait that can give up
+    // parts of a split tile, between the CTAs of a cluster: red_full the parts
+    // of the tokens this CTA sums have arrived, red_empty every CTA has summed
+    // its tokens (the buffers may be written again)
+    uint64_t red_full, red_empty;
     alignas(16) float sc[STAGES][NT];  // (read as float4) token scale * block scale
     uint32_t tmem;
     volatile int abort;
-    unsigned last;  // broadcast among the drain warps
 
-    // one warp
-    __device__ __forceinline__ void init(int lane) {
+    // one warp; ctas: CTAs that share a tile
+    __device__ __forceinline__ void init(int lane, int ctas) {
         if (lane < STAGES) {
             mbar_init(&w_full[lane], 1);
             mbar_init(&x_full[lane], 1);
@@ -181,7 +186,8 @@ struct Pipe {
         }
         if (lane == 0) {
             mbar_init(&mma_done, 1);
-            mbar_init(&drain_bar, D_WARPS);
+            mbar_init(&red_full, ctas * D_WARPS);
+            mbar_init(&red_empty, ctas * D_WARPS);
             abort = 0;
         }
     }
@@ -213,12 +219,15 @@ struct Pipe {
         __syncwarp();
         return __shfl_sync(0xffffffffu, ok, 0);
     }
-    // Barrier of the drain warps; phase counts the ones passed.  Not bar.sync:
-    // a drain warp that gave up elsewhere would leave the others waiting.
-    __device__ __forceinline__ bool drain_sync(uint32_t &phase, unsigned *err) {
+    // on a barrier that other CTAs of the cluster arrive on
+    __device__ __forceinline__ bool wait_warp_cluster(uint64_t *bar, uint32_t parity, unsigned *err) {
+        bool ok = true;
+        if ((threadIdx.x & 31) == 0) {
+            ok = sm100::mbar_wait_cluster(bar, parity, WAIT_CYCLES);
+            if (!ok) fail(err);
+        }
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&drain_bar);
-        return wait_warp(&drain_bar, phase++ & 1, err);
+        return __shfl_sync(0xffffffffu, ok, 0);
     }
 };
 
@@ -315,6 +324,16 @@ __device__ __forceinline__ bool pipe_drain(Pipe<NT> &p, uint32_t it, int quadran
     __syncwarp();
     if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&p.empty[s]);
     return true;
+}
+
+// Address of this CTA's shared memory location `local` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote_smem(const void *local, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(local)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_remote(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // Blocks dealt out evenly: CTA c of G owns [c total / G, (c + 1) total / G).

@@ -53,26 +53,28 @@ cudaError_t launch_fp8_pack(const Fp8PackParams &p, cudaStream_t s);
 cudaError_t launch_fp8_dequant(const uint8_t *tiles, const float *scale, float *w, int m, int n, int KB,
                                cudaStream_t s);
 
-// y [B][m] = x W^T on 128-row x NT-token tiles, the K blocks of all tiles
-// dealt out evenly over the CTAs
+// y [B][m] = x W^T on 128-row x NT-token tiles, clusters of C CTAs splitting K
 struct Fp8SkinnyParams {
     const uint8_t *w;
     const float *ws;
-    const void *x;      // source 0 / 1: f16 / bf16 [B][n], quantised on the way
-    const uint8_t *q;   // source 2: e4m3 [B][KB * 128] and
-    const float *s;     //           its scales [KB][s_ld]
+    const void *x;      // source 0 / 1: f16 / bf16 [B][n], rounded on the way
+    const float *s;     // source 2: scales [KB][s_ld] of the rows in qmap
     int64_t s_ld;
     void *y;
     int y_dtype;
     int m, n, B, RT, KB, TT;  // TT token tiles
-    float *part;        // [grid][2][NT][128]
-    unsigned *cnt;      // [RT * TT], zero between calls
+    int C;              // CTAs per cluster, 1..8, at most KB
     unsigned *err;
 };
 int fp8_skinny_tile(int64_t B);  // NT: tokens per tile for a batch of B
-size_t fp8_skinny_part_bytes(int nt, int grid);
+// clusters of c = 1..8 CTAs (one per SM) the current device holds at once
+cudaError_t fp8_skinny_clusters(int num_sms, int count[9]);
+struct Fp8SkinnyPlan {
+    int C, clusters;
+};
+Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, const int clusters[9]);
 // qmap: source 2 only, boxes of 128 columns x nt tokens of q, 128-byte swizzle
-cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, const CUtensorMap &qmap, int source, int nt, int grid,
+cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, const CUtensorMap &qmap, int source, int nt, int clusters,
                               cudaStream_t s, bool pdl);
 
 }  // namespace glq

@@ -67,7 +67,6 @@ void free_fp8(glq_fp8 L) {
     cudaFree(L->d_w);
     cudaFree(L->d_ws);
     cudaFree(L->d_err);
-    cudaFree(L->d_cnt);
     delete L;
 }
 
@@ -78,13 +77,9 @@ bool rounds_inside(int64_t B) { return B <= 4; }
 // What a call of B tokens needs of the shared workspace.
 void fp8_need(glq_fp8 L, int64_t B, bool quantized, size_t need[glq::FP8_WS_COUNT]) {
     B = std::min(B, MAX_SLICE);
-    if (B <= 0) return;
-    const int nt = glq::fp8_skinny_tile(B);
-    if (!quantized && !rounds_inside(B)) {
-        need[glq::FP8_WS_Q] = std::max(need[glq::FP8_WS_Q], (size_t)B * L->KB * GLQ_FP8_BLOCK);
-        need[glq::FP8_WS_S] = std::max(need[glq::FP8_WS_S], (size_t)B * L->KB * sizeof(float));
-    }
-    need[glq::FP8_WS_PART] = std::max(need[glq::FP8_WS_PART], glq::fp8_skinny_part_bytes(nt, L->num_sms));
+    if (B <= 0 || quantized || rounds_inside(B)) return;
+    need[glq::FP8_WS_Q] = std::max(need[glq::FP8_WS_Q], (size_t)B * L->KB * GLQ_FP8_BLOCK);
+    need[glq::FP8_WS_S] = std::max(need[glq::FP8_WS_S], (size_t)B * L->KB * sizeof(float));
 }
 
 // One slice of at most MAX_SLICE tokens: x (f16 / bf16), or q and s.
@@ -116,7 +111,6 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
     p.w = L->d_w;
     p.ws = L->d_ws;
     p.x = x;
-    p.q = q;
     p.s = s;
     p.s_ld = s_ld;
     p.y = y;
@@ -127,17 +121,15 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
     p.RT = L->RT;
     p.KB = L->KB;
     p.TT = (int)((B + nt - 1) / nt);
-    p.part = static_cast<float *>(buf[glq::FP8_WS_PART]);
-    p.cnt = L->d_cnt;
     p.err = L->d_err;
-    const int64_t total = (int64_t)p.RT * p.TT * p.KB;
-    const int grid = (int)std::min<int64_t>(L->num_sms, total);
+    const glq::Fp8SkinnyPlan plan = glq::plan_fp8_skinny((int64_t)p.RT * p.TT, p.KB, L->clusters);
+    p.C = plan.C;
     CUtensorMap qmap{};
     if (source == 2 && !encode_rows(&qmap, q, (int64_t)L->KB * GLQ_FP8_BLOCK, B, nt)) return GLQ_ERR_CUDA;
-    return launched(glq::launch_fp8_skinny(p, qmap, source, nt, grid, st, true));
+    return launched(glq::launch_fp8_skinny(p, qmap, source, nt, plan.clusters, st, true));
 }
 
-glq_status check_word(unsigned *d_err, unsigned *d_cnt, size_t cnt_bytes, cudaStream_t s) {
+glq_status check_word(unsigned *d_err, cudaStream_t s) {
     if (cudaStreamSynchronize(s) != cudaSuccess) {
         cudaGetLastError();
         return GLQ_ERR_CUDA;
@@ -145,9 +137,7 @@ glq_status check_word(unsigned *d_err, unsigned *d_cnt, size_t cnt_bytes, cudaSt
     unsigned err = 0;
     if (cudaMemcpy(&err, d_err, sizeof err, cudaMemcpyDeviceToHost) != cudaSuccess) return GLQ_ERR_CUDA;
     if (!err) return GLQ_OK;
-    // a call that gave up may have left its arrival counters half way
     cudaMemset(d_err, 0, sizeof(unsigned));
-    cudaMemset(d_cnt, 0, cnt_bytes);
     return (err & GLQ_DEVERR_TIMEOUT) ? GLQ_ERR_TIMEOUT : GLQ_ERR_DEVICE_CHECK;
 }
 
@@ -189,17 +179,16 @@ glq_status glq_fp8_create(int64_t m, int64_t n, const void *w_dev, int64_t ldw, 
     L->RT = (int)blocks_of(m);
     L->KB = (int)blocks_of(n);
     const int64_t tiles = (int64_t)L->RT * L->KB;
-    L->cnt_bytes = (size_t)L->RT * (MAX_SLICE / 128) * sizeof(unsigned);
     glq_status st = GLQ_OK;
     if (cudaGetDevice(&L->device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&L->num_sms, cudaDevAttrMultiProcessorCount, L->device) != cudaSuccess) {
+        cudaDeviceGetAttribute(&L->num_sms, cudaDevAttrMultiProcessorCount, L->device) != cudaSuccess ||
+        glq::fp8_skinny_clusters(L->num_sms, L->clusters) != cudaSuccess) {
         cudaGetLastError();
         st = GLQ_ERR_CUDA;
     }
     if (st == GLQ_OK) st = dev_alloc(&L->d_w, (size_t)tiles * GLQ_FP8_TILE_BYTES, &L->device_bytes);
     if (st == GLQ_OK) st = dev_alloc(&L->d_ws, (size_t)tiles * sizeof(float), &L->device_bytes);
     if (st == GLQ_OK) st = dev_alloc(&L->d_err, sizeof(unsigned), &L->device_bytes);
-    if (st == GLQ_OK) st = dev_alloc(&L->d_cnt, L->cnt_bytes, &L->device_bytes);
     if (st == GLQ_OK) {
         glq::Fp8PackParams p{};
         p.src = static_cast<const uint8_t *>(w_dev);
@@ -214,7 +203,6 @@ glq_status glq_fp8_create(int64_t m, int64_t n, const void *w_dev, int64_t ldw, 
         p.count = 1;
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         if (cudaMemsetAsync(L->d_err, 0, sizeof(unsigned), s) != cudaSuccess ||
-            cudaMemsetAsync(L->d_cnt, 0, L->cnt_bytes, s) != cudaSuccess ||
             glq::launch_fp8_pack(p, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess) {
             cudaGetLastError();
             st = GLQ_ERR_CUDA;
@@ -240,7 +228,7 @@ glq_status glq_fp8_reserve(glq_fp8 layer, int64_t max_B) {
     if (max_B < 0) return GLQ_ERR_SHAPE;
     DeviceGuard guard(layer->device);
     size_t need[glq::FP8_WS_COUNT] = {};
-    for (int64_t B : {(int64_t)16, (int64_t)32, (int64_t)64, max_B}) fp8_need(layer, std::min(B, max_B), false, need);
+    fp8_need(layer, max_B, false, need);
     void *buf[glq::FP8_WS_COUNT];
     return glq::fp8_workspace(layer->device, need, 0, buf);
 }
@@ -294,7 +282,7 @@ glq_status glq_fp8_dequant(glq_fp8 L, float *w_dev, void *stream) {
 glq_status glq_fp8_check(glq_fp8 L, void *stream) {
     if (!L) return GLQ_ERR_INVALID_ARG;
     DeviceGuard guard(L->device);
-    return check_word(L->d_err, L->d_cnt, L->cnt_bytes, static_cast<cudaStream_t>(stream));
+    return check_word(L->d_err, static_cast<cudaStream_t>(stream));
 }
 
 glq_status glq_fp8_info(glq_fp8 L, int64_t *m, int64_t *n, size_t *device_bytes) {

@@ -110,8 +110,7 @@ struct glq_fp8_s {
     uint8_t *d_w = nullptr;       // [RT][KB] operand tiles (glq_fp8.h)
     float *d_ws = nullptr;        // [RT][KB]
     unsigned *d_err = nullptr;
-    unsigned *d_cnt = nullptr;    // output-tile arrival counters, zero between calls
-    size_t cnt_bytes = 0;
+    int clusters[9] = {};         // clusters of 1..8 CTAs the device holds at once
     size_t device_bytes = 0;
 };
 
@@ -132,8 +131,8 @@ struct DeviceGuard {
 };
 
 // The 8-bit float operators' buffers in the device's shared workspace:
-// rounded activations, their scales, partial sums, expert activations.
-enum Fp8Ws { FP8_WS_Q, FP8_WS_S, FP8_WS_PART, FP8_WS_H, FP8_WS_COUNT };
+// rounded activations and their scales.
+enum Fp8Ws { FP8_WS_Q, FP8_WS_S, FP8_WS_COUNT };
 // Makes each at least need[i] bytes (the rules of the shared workspace hold:
 // growth synchronises, and is refused during stream capture).
 glq_status fp8_workspace(int dev, const size_t need[FP8_WS_COUNT], cudaStream_t s, void *out[FP8_WS_COUNT]);
