@@ -138,7 +138,7 @@ template <int NT, int SOURCE>
 __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __grid_constant__ CUtensorMap qmap,
                                                                      Fp8SkinnyParams p) {
     constexpr bool ROUND = SOURCE != 2;
-    constexpr int HALF = NT / 2, STAGES = Pipe<NT>::STAGES;
+    constexpr int HALF = NT / 2, STAGES = Pipe<NT>::STAGES, DRAIN = Pipe<NT>::DRAIN;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) Pipe<NT> pipe;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -161,18 +161,21 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
     sm100::tc_fence_after();
     pdl_launch_dependents();
 
-    uint32_t it = 0;  // warp 0: blocks whose copies have been started
+    uint32_t it = 0;  // the copy thread: blocks whose copies have been started
+    bool copier = false;
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
+            copier = true;
+            const uint64_t policy = evict_first_policy();
             uint32_t t = first, k = 0, xt = first, xk = 0;
             auto load_w = [&]() {
                 const uint8_t *w = p.w + ((int64_t)(t / TT) * p.KB + k0 + k) * GLQ_FP8_TILE_BYTES;
-                if (!pipe_load<NT, ROUND>(pipe, smem, it, w, ROUND ? 0 : NT * 128, p.err)) return false;
+                if (!pipe_load<NT, ROUND>(pipe, smem, it, w, ROUND ? 0 : NT * 128, policy, p.err)) return false;
                 if (++k == nk) k = 0, t += NC;
                 return true;
             };
             auto load_x = [&](uint32_t i) {
-                sm100::tma_load_2d(pipe_x_tile<NT>(smem, i), &qmap, &pipe.w_full[i % STAGES],
+                sm100::tma_load_2d(pipe_x_tile<NT>(smem, i), &qmap, &pipe.full[i % STAGES],
                                    (int)(k0 + xk) * GLQ_FP8_BLOCK, (int)(xt % TT) * NT);
                 if (++xk == nk) xk = 0, xt += NC;
             };
@@ -191,36 +194,70 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            pipe_mma<NT, ROUND>(pipe, smem, 0, nblk, p.err);
+        if (elect_one()) {
+            pipe_mma<NT>(pipe, smem, 0, nblk, p.err);
             sm100::mma_commit(&pipe.mma_done);  // every MMA issued has completed
             sm100::mbar_wait(&pipe.mma_done, 0, WAIT_CYCLES);
         }
     } else if (warp < D_WARP0) {
         pdl_wait();
-        for (uint32_t i = warp - X_WARP0; i < nblk && warp < X_WARP0 + Pipe<NT>::X_TURN; i += Pipe<NT>::X_TURN) {
+        // Everything a block needs from memory is loaded one turn ahead (the
+        // block scales come from DRAM, behind the weights in flight) and
+        // rounded before its stage is waited for: a load after the wait would
+        // add its trip to the time a stage takes to come round (0.37 us a
+        // block for 11 stages, whatever the number of SMs).
+        using T = typename std::conditional<SOURCE == 0, __half, __nv_bfloat16>::type;
+        constexpr int ROWS = ROUND ? FP8_ROUND_MAX : 1, SC = (NT + 31) / 32;
+        struct Ahead {
+            uint2 x[ROWS];
+            float s[SC], ws;
+        } a;
+        const uint32_t turn = Pipe<NT>::X_TURN;
+        auto fetch = [&](uint32_t i, Ahead &f) {
+            if (i >= nblk) return;
             const uint32_t q = i / nk, t = first + q * NC, k = k0 + (i - q * nk), rt = t / TT;
             const int tok0 = (int)(t - rt * TT) * NT, live = min(NT, p.B - tok0);
-            const float ws = __ldg(p.ws + (int64_t)rt * p.KB + k);
-            float *sc = pipe.sc[i % STAGES];
-            if constexpr (ROUND) {
-                using T = typename std::conditional<SOURCE == 0, __half, __nv_bfloat16>::type;
+            f.ws = __ldg(p.ws + (int64_t)rt * p.KB + k);
+            if constexpr (ROUND) {  // TT is 1
                 const int col = k * GLQ_FP8_BLOCK + lane * 4;
-                if (!pipe_x_begin(pipe, i, p.err)) break;
-                // n is a multiple of 8: a lane's four columns are in or out together
-                warp_quantize_rows(static_cast<const T *>(p.x) + (int64_t)tok0 * p.n + col, (int64_t)p.n, col < p.n, live,
-                                   pipe_x_tile<NT>(smem, i), sc, ws, lane);
-            } else {
-                float s[(NT + 31) / 32];
+                const T *src = static_cast<const T *>(p.x) + col;
 #pragma unroll
-                for (int j = 0; j < (NT + 31) / 32; ++j) {
-                    const int tok = j * 32 + lane;
-                    s[j] = tok < live ? p.s[(int64_t)k * p.s_ld + tok0 + tok] * ws : 0.f;
+                for (int r = 0; r < ROWS; ++r) {
+                    f.x[r] = make_uint2(0, 0);
+                    // n is a multiple of 8: a lane's four columns are in or out together
+                    if (r < live && col < p.n) f.x[r] = __ldg(reinterpret_cast<const uint2 *>(src + (int64_t)r * p.n));
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < SC; ++j) {
+                    const int tok = j * 32 + lane;
+                    f.s[j] = tok < live ? p.s[(int64_t)k * p.s_ld + tok0 + tok] : 0.f;
+                }
+            }
+        };
+        const uint32_t w0 = warp - X_WARP0;
+        if (w0 < turn) fetch(w0, a);
+        for (uint32_t i = w0; i < nblk && w0 < turn; i += turn) {
+            float *sc = pipe.sc[i % STAGES];
+            const Ahead f = a;
+            fetch(i + turn, a);
+            if constexpr (ROUND) {
+                uint32_t q[ROWS];
+                float s[ROWS];
+                warp_quantize_rows<T, ROWS>(f.x, p.B, q, s);
+                if (!pipe_x_begin(pipe, i, p.err)) break;
+                uint8_t *xt = pipe_x_tile<NT>(smem, i);
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    if (r >= p.B) break;
+                    *reinterpret_cast<uint32_t *>(xt + sw128(r, lane >> 2) + (lane & 3) * 4) = q[r];
+                    if (lane == 0) sc[r] = s[r] * f.ws;
+                }
+            } else {
                 if (!pipe_x_begin(pipe, i, p.err)) break;
 #pragma unroll
-                for (int j = 0; j < (NT + 31) / 32; ++j)
-                    if (j * 32 + lane < NT) sc[j * 32 + lane] = s[j];
+                for (int j = 0; j < SC; ++j)
+                    if (j * 32 + lane < NT) sc[j * 32 + lane] = f.s[j] * f.ws;
             }
             pipe_x_done<NT, ROUND>(pipe, i, lane);
         }
@@ -237,8 +274,13 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
 #pragma unroll
             for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
             bool ok = true;
-            for (uint32_t k = 0; k < nk && ok; ++k, ++i)
-                ok = pipe_drain<NT, false>(pipe, i, quadrant, set, acc, p.err);
+            for (uint32_t k = 0; k < nk && ok;) {
+                const int n = min((int)(nk - k), DRAIN);
+                if (n == DRAIN) ok = pipe_drain<NT, DRAIN, false>(pipe, i, quadrant, set, acc, p.err);
+                else ok = pipe_drain<NT, 1, false>(pipe, i, quadrant, set, acc, p.err);
+                k += n == DRAIN ? DRAIN : 1;
+                i += n == DRAIN ? DRAIN : 1;
+            }
             if (!ok) break;
             if (C == 1) {
                 const int row = rt * 128 + row_l;
@@ -277,7 +319,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
     }
     sm100::tc_fence_before();
     __syncthreads();
-    if (tid == 0 && pipe.abort) pipe_load_drain(pipe, it);
+    if (copier && pipe.abort) pipe_load_drain(pipe, it);
     __syncwarp();
     if (warp == 1) {
         sm100::tc_fence_after();
@@ -286,12 +328,6 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
     if (C > 1) sm100::cluster_sync_all();  // no CTA leaves while another may still write to it
 }
 
-template <int NT>
-const void *skinny_fn(int source) {
-    return source == 0   ? (const void *)fp8_skinny_kernel<NT, 0>
-           : source == 1 ? (const void *)fp8_skinny_kernel<NT, 1>
-                         : (const void *)fp8_skinny_kernel<NT, 2>;
-}
 
 }  // namespace
 
@@ -328,17 +364,20 @@ struct SkinnyKernel {
 };
 
 SkinnyKernel skinny_kernel(int source, int nt) {
+    if (source < 2)  // at most FP8_ROUND_MAX tokens
+        return {source ? (const void *)fp8_skinny_kernel<16, 1> : (const void *)fp8_skinny_kernel<16, 0>,
+                Pipe<16>::SMEM_BYTES, source};
     switch (nt) {
-        case 16: return {skinny_fn<16>(source), Pipe<16>::SMEM_BYTES, source};
-        case 32: return {skinny_fn<32>(source), Pipe<32>::SMEM_BYTES, 3 + source};
-        case 64: return {skinny_fn<64>(source), Pipe<64>::SMEM_BYTES, 6 + source};
-        default: return {skinny_fn<128>(source), Pipe<128>::SMEM_BYTES, 9 + source};
+        case 16: return {(const void *)fp8_skinny_kernel<16, 2>, Pipe<16>::SMEM_BYTES, 2};
+        case 32: return {(const void *)fp8_skinny_kernel<32, 2>, Pipe<32>::SMEM_BYTES, 3};
+        case 64: return {(const void *)fp8_skinny_kernel<64, 2>, Pipe<64>::SMEM_BYTES, 4};
+        default: return {(const void *)fp8_skinny_kernel<128, 2>, Pipe<128>::SMEM_BYTES, 5};
     }
 }
 
 // Sets the kernel's shared memory limit once per device.
 cudaError_t prepare(const SkinnyKernel &k) {
-    static std::atomic<uint64_t> configured[12];
+    static std::atomic<uint64_t> configured[6];
     return once_per_device(configured[k.key], [&k] {
         return cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
     });

@@ -64,31 +64,17 @@ __device__ __forceinline__ uint32_t warp_quantize(const float v[4], float &scale
 // with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
 
-// The same for `live` rows of x (n columns, this block's from `col`; in: the
-// lane's columns exist), written as the swizzled operand tile xt, with the
-// scales times `ws`.  Eight rows are loaded before the first is rounded: one
-// at a time, each would cost a trip to L2 (13 tokens of 14336 columns: 2600
-// cycles a block).
-template <typename T>
-__device__ __forceinline__ void warp_quantize_rows(const T *src, int64_t ld, bool in, int live, uint8_t *xt, float *sc,
-                                                   float ws, int lane) {
-    for (int r0 = 0; r0 < live; r0 += 8) {
-        uint2 w[8];
+// The same for up to ROWS rows of x, in registers: q[r] the packed values of
+// row r, scale[r] its scale.  All rows are loaded before the first is rounded.
+template <typename T, int ROWS>
+__device__ __forceinline__ void warp_quantize_rows(const uint2 (&w)[ROWS], int live, uint32_t (&q)[ROWS],
+                                                   float (&scale)[ROWS]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[i] = make_uint2(0, 0);
-            if (in && r0 + i < live) w[i] = __ldg(reinterpret_cast<const uint2 *>(src + (int64_t)(r0 + i) * ld));
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (r0 + i >= live) break;
-            const float2 a = unpack2<T>(w[i].x), c = unpack2<T>(w[i].y);
-            const float v[4] = {a.x, a.y, c.x, c.y};
-            float s;
-            const uint32_t q = warp_quantize(v, s);
-            *reinterpret_cast<uint32_t *>(xt + sw128(r0 + i, lane >> 2) + (lane & 3) * 4) = q;
-            if (lane == 0) sc[r0 + i] = s * ws;
-        }
+    for (int r = 0; r < ROWS; ++r) {
+        if (r >= live) break;
+        const float2 a = unpack2<T>(w[r].x), c = unpack2<T>(w[r].y);
+        const float v[4] = {a.x, a.y, c.x, c.y};
+        q[r] = warp_quantize(v, scale[r]);
     }
 }
 
@@ -120,6 +106,32 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t r[8]) {
                  : "r"(taddr));
 }
 
+// True in one lane of a converged warp.  Copies, MMAs and commits take uniform
+// operands: behind elect.sync the compiler knows that one lane is left, behind
+// a test of the lane number it does not, and a wait + copy or MMA iteration
+// takes twice as long (500 against 250 cycles).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
+// 1-D bulk copy of weights, which pass through L2 once: first to be evicted
+// (measured: 6.2 against 5.8 TB/s over 600 MB).
+__device__ __forceinline__ uint64_t evict_first_policy() {
+    uint64_t r;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(r));
+    return r;
+}
+__device__ __forceinline__ void bulk_g2s_once(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                              uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_addr(dst)),
+        "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // The few-token pipeline.  The weights are the MMA's M side (128 rows), up to
 // NT tokens its N side, one MMA group per 128-column block (K = 128: four
@@ -134,9 +146,8 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t r[8]) {
 //   warps 10-17  drain: warp & 3 is its TMEM lane quadrant (rows), the two
 //                sets of four take half of the tokens each
 // A stage is one weight tile, its token tile, its scales and its TMEM slot;
-// four barriers carry it round:
-//   w_full the copies have landed -> MMA
-//   x_full the scales (and the tile rounded on the way) are written -> drain (MMA)
+// three barriers carry it round:
+//   full   the copies have landed and the scale warp has written -> MMA
 //   done   the MMA has finished -> drain (weight copy of the next use)
 //   empty  the drain has read it -> everything of the next use
 // One commit per block and one polling lane per warp: with stages and slots
@@ -157,6 +168,7 @@ struct Pipe {
     static constexpr int TMEM_COLS = NT == 16 ? 256 : 512;
     static_assert(STAGES * NT <= TMEM_COLS, "a slot per stage");
     static constexpr int HALF = NT / 2;     // tokens of one drain set
+    static constexpr int DRAIN = NT == 16 ? 4 : NT == 32 ? 2 : 1;  // blocks a drain warp takes at once
     // Token-operand warps in turn.  A warp's next block is X_TURN after its
     // last, whose begin showed block (last - STAGES) drained; the parity of a
     // barrier tells phases apart only one back, so X_TURN may not exceed the
@@ -167,7 +179,7 @@ struct Pipe {
     static constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + RED_BYTES;
     static_assert(SMEM_BYTES + 4096 <= 227 * 1024, "shared memory");
 
-    uint64_t w_full[STAGES], x_full[STAGES], done[STAGES], empty[STAGES], mma_done;
+    uint64_t full[STAGES], done[STAGES], empty[STAGES], mma_done;
     // parts of a split tile, between the CTAs of a cluster: red_full the parts
     // of the tokens this CTA sums have arrived, red_empty every CTA has summed
     // its tokens (the buffers may be written again)
@@ -179,8 +191,7 @@ struct Pipe {
     // one warp; ctas: CTAs that share a tile
     __device__ __forceinline__ void init(int lane, int ctas) {
         if (lane < STAGES) {
-            mbar_init(&w_full[lane], 1);
-            mbar_init(&x_full[lane], 1);
+            mbar_init(&full[lane], 2);
             mbar_init(&done[lane], 1);
             mbar_init(&empty[lane], D_WARPS);
         }
@@ -238,11 +249,11 @@ struct Pipe {
 // TMEM slot is waited for here.
 template <int NT, bool X_WRITTEN>
 __device__ __forceinline__ bool pipe_load(Pipe<NT> &p, uint8_t *smem, uint32_t it, const uint8_t *tile, uint32_t extra,
-                                          unsigned *err) {
+                                          uint64_t policy, unsigned *err) {
     const uint32_t s = it % Pipe<NT>::STAGES, use = it / Pipe<NT>::STAGES;
     if (!p.wait(X_WRITTEN ? &p.done[s] : &p.empty[s], (use & 1) ^ 1, err)) return false;
-    mbar_expect_tx(&p.w_full[s], GLQ_FP8_TILE_BYTES + extra);
-    bulk_g2s(smem + s * Pipe<NT>::STAGE_BYTES, tile, GLQ_FP8_TILE_BYTES, &p.w_full[s]);
+    mbar_expect_tx(&p.full[s], GLQ_FP8_TILE_BYTES + extra);
+    bulk_g2s_once(smem + s * Pipe<NT>::STAGE_BYTES, tile, GLQ_FP8_TILE_BYTES, &p.full[s], policy);
     return true;
 }
 template <int NT>
@@ -251,23 +262,23 @@ __device__ __forceinline__ uint8_t *pipe_x_tile(uint8_t *smem, uint32_t it) {
 }
 
 // Before the CTA exits, if it gave up: let the copies of the last blocks land
-// (`loaded` blocks were issued; an earlier use of a stage has landed, or it
-// would not have been loaded again).
+// (`loaded` blocks were started; an earlier use of a stage has landed, or it
+// would not have been loaded again).  A block whose scale warp stopped never
+// completes: its wait runs out, long after any copy has landed.
 template <int NT>
 __device__ __forceinline__ void pipe_load_drain(Pipe<NT> &p, uint32_t loaded) {
     for (uint32_t i = loaded > (uint32_t)Pipe<NT>::STAGES ? loaded - Pipe<NT>::STAGES : 0; i < loaded; ++i)
-        sm100::mbar_wait(&p.w_full[i % Pipe<NT>::STAGES], (i / Pipe<NT>::STAGES) & 1, WAIT_CYCLES);
+        sm100::mbar_wait(&p.full[i % Pipe<NT>::STAGES], (i / Pipe<NT>::STAGES) & 1, WAIT_CYCLES / 64);
 }
 
-// The MMA warp's one thread: blocks [it, it + count).  X_WRITTEN: the token
-// tile is written by a warp rather than copied.
-template <int NT, bool X_WRITTEN>
+// The MMA warp's one thread: blocks [it, it + count).
+template <int NT>
 __device__ __forceinline__ bool pipe_mma(Pipe<NT> &p, uint8_t *smem, uint32_t it, uint32_t count, unsigned *err) {
     const uint32_t idesc = idesc_e4m3_f32(128, NT);
     const uint32_t tmem = p.tmem;
     uint32_t s = it % Pipe<NT>::STAGES, par = (it / Pipe<NT>::STAGES) & 1;
     for (uint32_t i = 0; i < count; ++i) {
-        if ((X_WRITTEN && !p.wait(&p.x_full[s], par, err)) || !p.wait(&p.w_full[s], par, err)) return false;
+        if (!p.wait(&p.full[s], par, err)) return false;
         sm100::tc_fence_after();
         uint8_t *st = smem + s * Pipe<NT>::STAGE_BYTES;
         const uint64_t a = sm100::smem_desc_sw128(st), b = sm100::smem_desc_sw128(st + GLQ_FP8_TILE_BYTES);
@@ -289,40 +300,55 @@ template <int NT, bool X_WRITTEN>
 __device__ __forceinline__ void pipe_x_done(Pipe<NT> &p, uint32_t it, int lane) {
     if (X_WRITTEN) sm100::fence_proxy_async_smem();  // the MMA reads the tile through the async proxy
     __syncwarp();
-    if (lane == 0) sm100::mbar_arrive(&p.x_full[it % Pipe<NT>::STAGES]);
+    if (lane == 0) sm100::mbar_arrive(&p.full[it % Pipe<NT>::STAGES]);
 }
 
-// A drain warp: adds block `it` to acc (its half of the tokens).  SKIP_ZERO:
-// tokens whose scale is 0 take no part (their operand rows are not written).
-template <int NT, bool SKIP_ZERO>
+// A drain warp: adds blocks it .. it + N - 1 to acc (its half of the tokens).
+// The last block's wait covers the others (MMAs complete in order); several
+// blocks share its cost, about 300 cycles for wait, TMEM load and arrive.
+// SKIP_ZERO: tokens whose scale is 0 take no part (their operand rows are not
+// written).
+template <int NT, int N, bool SKIP_ZERO>
 __device__ __forceinline__ bool pipe_drain(Pipe<NT> &p, uint32_t it, int quadrant, int set, float (&acc)[NT / 2],
                                            unsigned *err) {
-    constexpr int HALF = NT / 2;
+    constexpr int HALF = NT / 2, STAGES = Pipe<NT>::STAGES;
     constexpr int STEP = HALF < 16 ? 8 : 16;
-    const uint32_t s = it % Pipe<NT>::STAGES, par = (it / Pipe<NT>::STAGES) & 1;
-    if (!p.wait_warp(&p.done[s], par, err) || !p.wait_warp(&p.x_full[s], par, err)) return false;
+    const uint32_t last = it + N - 1;
+    if (!p.wait_warp(&p.done[last % STAGES], (last / STAGES) & 1, err)) return false;
     sm100::tc_fence_after();
-    const uint32_t t0 = p.tmem + ((uint32_t)(32 * quadrant) << 16) + s * NT + set * HALF;
-    const float4 *sc = reinterpret_cast<const float4 *>(&p.sc[s][set * HALF]);
+    const uint32_t t0 = p.tmem + ((uint32_t)(32 * quadrant) << 16) + set * HALF;
+    uint32_t s[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) s[n] = (it + n) % STAGES;
 #pragma unroll
     for (int c = 0; c < HALF; c += STEP) {
-        uint32_t d[STEP];
-        if constexpr (STEP == 8) tmem_ld8(t0 + c, d);
-        else sm100::tmem_ld16(t0 + c, d);
+        uint32_t d[N][STEP];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            if constexpr (STEP == 8) tmem_ld8(t0 + s[n] * NT + c, d[n]);
+            else sm100::tmem_ld16(t0 + s[n] * NT + c, d[n]);
+        }
         sm100::tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < STEP; j += 4) {
-            const float4 f = sc[(c + j) >> 2];
-            const float fs[4] = {f.x, f.y, f.z, f.w};
+        for (int n = 0; n < N; ++n) {
+            const float4 *sc = reinterpret_cast<const float4 *>(&p.sc[s[n]][set * HALF + c]);
 #pragma unroll
-            for (int l = 0; l < 4; ++l)
-                if (!SKIP_ZERO || fs[l] != 0.f)
-                    acc[c + j + l] = fmaf(__uint_as_float(d[j + l]), fs[l], acc[c + j + l]);
+            for (int j = 0; j < STEP; j += 4) {
+                const float4 f = sc[j >> 2];
+                const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int l = 0; l < 4; ++l)
+                    if (!SKIP_ZERO || fs[l] != 0.f)
+                        acc[c + j + l] = fmaf(__uint_as_float(d[n][j + l]), fs[l], acc[c + j + l]);
+            }
         }
     }
     sm100::tc_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&p.empty[s]);
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) sm100::mbar_arrive(&p.empty[s[n]]);
+    }
     return true;
 }
 

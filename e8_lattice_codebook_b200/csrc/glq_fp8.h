@@ -66,6 +66,7 @@ struct Fp8SkinnyParams {
     int C;              // CTAs per cluster, 1..8, at most KB
     unsigned *err;
 };
+constexpr int FP8_ROUND_MAX = 4;  // most tokens of sources 0 and 1
 int fp8_skinny_tile(int64_t B);  // NT: tokens per tile for a batch of B
 // clusters of c = 1..8 CTAs (one per SM) the current device holds at once
 cudaError_t fp8_skinny_clusters(int num_sms, int count[9]);

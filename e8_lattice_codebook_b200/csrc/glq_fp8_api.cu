@@ -72,7 +72,7 @@ void free_fp8(glq_fp8 L) {
 
 // Batches whose activations the product itself rounds; above, a kernel of
 // their own rounds them first.
-bool rounds_inside(int64_t B) { return B <= 4; }
+bool rounds_inside(int64_t B) { return B <= glq::FP8_ROUND_MAX; }
 
 // What a call of B tokens needs of the shared workspace.
 void fp8_need(glq_fp8 L, int64_t B, bool quantized, size_t need[glq::FP8_WS_COUNT]) {
