@@ -166,31 +166,35 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
     if (warp == 0) {
         if (elect_one()) {
             copier = true;
-            const uint64_t policy = evict_first_policy();
-            uint32_t t = first, k = 0, xt = first, xk = 0;
-            auto load_w = [&]() {
-                const uint8_t *w = p.w + ((int64_t)(t / TT) * p.KB + k0 + k) * GLQ_FP8_TILE_BYTES;
-                if (!pipe_load<NT, ROUND>(pipe, smem, it, w, ROUND ? 0 : NT * 128, policy, p.err)) return false;
-                if (++k == nk) k = 0, t += NC;
-                return true;
-            };
-            auto load_x = [&](uint32_t i) {
-                sm100::tma_load_2d(pipe_x_tile<NT>(smem, i), &qmap, &pipe.full[i % STAGES],
-                                   (int)(k0 + xk) * GLQ_FP8_BLOCK, (int)(xt % TT) * NT);
-                if (++xk == nk) xk = 0, xt += NC;
-            };
-            if (!ROUND) sm100::prefetch_tensormap(&qmap);
+            Loader<NT> ld(smem);
             // weights are constant: the first copies do not wait for the kernel
             // before, which the rounded tokens come from
-            const uint32_t n = min(nblk, (uint32_t)STAGES);
-            for (; it < n; ++it) load_w();
-            if (!ROUND) {
-                pdl_wait();
-                for (uint32_t i = 0; i < n; ++i) load_x(i);
+            const uint32_t ahead = ROUND ? 0 : min(nblk, (uint32_t)STAGES);
+            for (uint32_t t = first; t < tiles && it < ahead; t += NC) {
+                const uint8_t *w = p.w + ((int64_t)(t / TT) * p.KB + k0) * GLQ_FP8_TILE_BYTES;
+                for (uint32_t k = 0; k < nk && it < ahead; ++k, ++it, w += GLQ_FP8_TILE_BYTES, ld.next())
+                    pipe_load<NT, ROUND>(pipe, ld, w, NT * 128, p.err);
             }
-            for (; it < nblk; ++it) {
-                if (!load_w()) break;
-                if (!ROUND) load_x(it);
+            if (!ROUND) {
+                sm100::prefetch_tensormap(&qmap);
+                pdl_wait();
+            }
+            uint32_t i = 0;
+            bool ok = true;
+            ld = Loader<NT>(smem);
+            for (uint32_t t = first; t < tiles && ok; t += NC) {
+                const uint32_t rt = t / TT;
+                const uint8_t *w = p.w + ((int64_t)rt * p.KB + k0) * GLQ_FP8_TILE_BYTES;
+                const int tok0 = (int)(t - rt * TT) * NT;
+                int col = (int)k0 * GLQ_FP8_BLOCK;
+                for (uint32_t k = 0; k < nk; ++k, ++i, w += GLQ_FP8_TILE_BYTES, col += GLQ_FP8_BLOCK, ld.next()) {
+                    if (i >= ahead) {
+                        ok = pipe_load<NT, ROUND>(pipe, ld, w, ROUND ? 0 : NT * 128, p.err);
+                        if (!ok) break;
+                        ++it;
+                    }
+                    if (!ROUND) sm100::tma_load_2d(ld.dst + GLQ_FP8_TILE_BYTES, &qmap, &pipe.full[ld.stage], col, tok0);
+                }
             }
         }
     } else if (warp == 1) {
@@ -200,6 +204,10 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
             sm100::mbar_wait(&pipe.mma_done, 0, WAIT_CYCLES);
         }
     } else if (warp < D_WARP0) {
+        // the block scales of this CTA come from DRAM, behind the weights in
+        // flight: into L2 before those are too many
+        for (uint32_t t = first + (warp - X_WARP0) * NC; t < tiles; t += X_WARPS * NC)
+            for (uint32_t k = lane * 32; k < nk; k += 32 * 32) prefetch_l2(p.ws + (int64_t)(t / TT) * p.KB + k0 + k);
         pdl_wait();
         // Everything a block needs from memory is loaded one turn ahead (the
         // block scales come from DRAM, behind the weights in flight) and
@@ -240,7 +248,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
         for (uint32_t i = w0; i < nblk && w0 < turn; i += turn) {
             float *sc = pipe.sc[i % STAGES];
             const Ahead f = a;
-            fetch(i + turn, a);
+            if constexpr (!ROUND) fetch(i + turn, a);
             if constexpr (ROUND) {
                 uint32_t q[ROWS];
                 float s[ROWS];
@@ -260,6 +268,8 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
                     if (j * 32 + lane < NT) sc[j * 32 + lane] = f.s[j] * f.ws;
             }
             pipe_x_done<NT, ROUND>(pipe, i, lane);
+            // not before: the proxy fence in pipe_x_done waits for loads in flight
+            if constexpr (ROUND) fetch(i + turn, a);
         }
     } else {
         pdl_wait();  // y may still be in use by the kernel before

@@ -168,7 +168,7 @@ struct Pipe {
     static constexpr int TMEM_COLS = NT == 16 ? 256 : 512;
     static_assert(STAGES * NT <= TMEM_COLS, "a slot per stage");
     static constexpr int HALF = NT / 2;     // tokens of one drain set
-    static constexpr int DRAIN = NT == 16 ? 4 : NT == 32 ? 2 : 1;  // blocks a drain warp takes at once
+    static constexpr int DRAIN = NT <= 32 ? 2 : 1;  // blocks a drain warp takes at once
     // Token-operand warps in turn.  A warp's next block is X_TURN after its
     // last, whose begin showed block (last - STAGES) drained; the parity of a
     // barrier tells phases apart only one back, so X_TURN may not exceed the
@@ -242,18 +242,33 @@ struct Pipe {
     }
 };
 
-// The copy thread, block `it`: waits for its stage and starts its weight tile;
-// extra: bytes that other copies will bring for the block.  Where the token
-// tile is written by a warp, that warp has waited for the drain and the copy
-// may start when the MMA has finished with the tile; else the drain of the
-// TMEM slot is waited for here.
+// The copy thread's place in the ring; it keeps running indices and pointers:
+// with a division or a remainder in its loop a copy took 570 cycles instead of
+// 300, and the copies in flight never covered the memory's latency.
+template <int NT>
+struct Loader {
+    uint32_t stage = 0, parity = 1;  // of the wait for the stage's last use
+    uint8_t *dst;                    // the stage's weight tile
+    uint8_t *smem;
+    uint64_t policy;
+    __device__ __forceinline__ explicit Loader(uint8_t *s) : dst(s), smem(s), policy(evict_first_policy()) {}
+    __device__ __forceinline__ void next() {
+        dst += Pipe<NT>::STAGE_BYTES;
+        if (++stage == Pipe<NT>::STAGES) stage = 0, parity ^= 1, dst = smem;
+    }
+};
+
+// The copy thread: waits for its stage and starts its weight tile; extra:
+// bytes that other copies will bring for the block.  Where the token tile is
+// written by a warp, that warp has waited for the drain and the copy may start
+// when the MMA has finished with the tile; else the drain of the TMEM slot is
+// waited for here.
 template <int NT, bool X_WRITTEN>
-__device__ __forceinline__ bool pipe_load(Pipe<NT> &p, uint8_t *smem, uint32_t it, const uint8_t *tile, uint32_t extra,
-                                          uint64_t policy, unsigned *err) {
-    const uint32_t s = it % Pipe<NT>::STAGES, use = it / Pipe<NT>::STAGES;
-    if (!p.wait(X_WRITTEN ? &p.done[s] : &p.empty[s], (use & 1) ^ 1, err)) return false;
-    mbar_expect_tx(&p.full[s], GLQ_FP8_TILE_BYTES + extra);
-    bulk_g2s_once(smem + s * Pipe<NT>::STAGE_BYTES, tile, GLQ_FP8_TILE_BYTES, &p.full[s], policy);
+__device__ __forceinline__ bool pipe_load(Pipe<NT> &p, const Loader<NT> &l, const uint8_t *tile, uint32_t extra,
+                                          unsigned *err) {
+    if (!p.wait(X_WRITTEN ? &p.done[l.stage] : &p.empty[l.stage], l.parity, err)) return false;
+    mbar_expect_tx(&p.full[l.stage], GLQ_FP8_TILE_BYTES + extra);
+    bulk_g2s_once(l.dst, tile, GLQ_FP8_TILE_BYTES, &p.full[l.stage], l.policy);
     return true;
 }
 template <int NT>
