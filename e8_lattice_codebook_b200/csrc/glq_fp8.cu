@@ -157,12 +157,12 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
     }
     sm100::tc_fence_before();
     __syncthreads();
-    if (C > 1) sm100::cluster_sync_all();  // barriers are set up before another CTA arrives on them
+    if (C > 1) cluster_arrive();  // the wait for the others' barriers is the drain's
     sm100::tc_fence_after();
     pdl_launch_dependents();
 
     uint32_t it = 0;  // the copy thread: blocks whose copies have been started
-    bool copier = false;
+    bool copier = false, met = false;  // met: has waited for the cluster's barriers to be set up
     if (warp == 0) {
         if (elect_one()) {
             copier = true;
@@ -303,18 +303,21 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
                 continue;
             }
             // parts to the CTAs that sum them
+            const int mine = live > (int)rank ? (live - (int)rank - 1) / (int)C + 1 : 0;  // tokens this CTA sums
+            if (!met) cluster_wait(), met = true;
             if (!pipe.wait_warp_cluster(&pipe.red_empty, (round & 1) ^ 1, p.err)) break;
+            if (dtid == 0) mbar_expect_tx(&pipe.red_full, (uint32_t)(mine * (int)C) * 512);
 #pragma unroll
             for (int j = 0; j < HALF; ++j) {
-                const int tok = set * HALF + j, own = tok / C;
-                if (tok < live) st_remote(remote_smem(red + ((int)rank * per + own) * 128 + row_l, tok - own * C), acc[j]);
+                const int tok = set * HALF + j, own = tok / C, to = tok - own * C;
+                if (tok < live)
+                    st_async(remote_smem(red + ((int)rank * per + own) * 128 + row_l, to), acc[j],
+                             remote_smem(&pipe.red_full, to));
             }
-            __syncwarp();
-            if (lane < C) sm100::mbar_arrive_remote(&pipe.red_full, lane);
             if (!pipe.wait_warp_cluster(&pipe.red_full, round & 1, p.err)) break;
             // a warp sums one token in eight, a lane four rows
             const int row = rt * 128 + lane * 4;
-            for (int own = dtid >> 5; own * (int)C + (int)rank < live; own += D_WARPS) {
+            for (int own = dtid >> 5; own < mine; own += D_WARPS) {
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (uint32_t c = 0; c < C; ++c) {
                     const float4 v = *reinterpret_cast<const float4 *>(red + ((int)c * per + own) * 128 + lane * 4);
@@ -324,9 +327,13 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
                 if (row < p.m) store_y4(p.y, p.y_dtype, (int64_t)(tok0 + own * (int)C + (int)rank) * p.m + row, sum);
             }
             __syncwarp();
-            if (lane < C) sm100::mbar_arrive_remote(&pipe.red_empty, lane);
+            // in the last round nobody waits for it, and a CTA may leave as soon
+            // as its own parts are here
+            if (t + NC < tiles && lane < C) sm100::mbar_arrive_remote(&pipe.red_empty, lane);
         }
     }
+    __syncwarp();
+    if (C > 1 && !met) cluster_wait();
     sm100::tc_fence_before();
     __syncthreads();
     if (copier && pipe.abort) pipe_load_drain(pipe, it);
@@ -335,7 +342,9 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
         sm100::tc_fence_after();
         sm100::tmem_dealloc(pipe.tmem, Pipe<NT>::TMEM_COLS);
     }
-    if (C > 1) sm100::cluster_sync_all();  // no CTA leaves while another may still write to it
+    // A CTA that has its parts is written to no more; one that gave up before
+    // waits for the others to finish or leave.
+    if (C > 1 && pipe.abort) sm100::cluster_sync_all();
 }
 
 

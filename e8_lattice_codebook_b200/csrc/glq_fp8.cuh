@@ -180,7 +180,7 @@ struct Pipe {
     static_assert(SMEM_BYTES + 4096 <= 227 * 1024, "shared memory");
 
     uint64_t full[STAGES], done[STAGES], empty[STAGES], mma_done;
-    // parts of a split tile, between the CTAs of a cluster: red_full the parts
+    // parts of a split tile, between the CTAs of a cluster: red_full the bytes
     // of the tokens this CTA sums have arrived, red_empty every CTA has summed
     // its tokens (the buffers may be written again)
     uint64_t red_full, red_empty;
@@ -197,7 +197,7 @@ struct Pipe {
         }
         if (lane == 0) {
             mbar_init(&mma_done, 1);
-            mbar_init(&red_full, ctas * D_WARPS);
+            mbar_init(&red_full, 1);
             mbar_init(&red_empty, ctas * D_WARPS);
             abort = 0;
         }
@@ -373,9 +373,16 @@ __device__ __forceinline__ uint32_t remote_smem(const void *local, uint32_t rank
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(local)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_remote(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Store into another CTA's shared memory that counts its 4 bytes on a barrier
+// there: the reader waits for the data itself, no store has to be
+// acknowledged before an arrival may follow it.
+__device__ __forceinline__ void st_async(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+                 "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Blocks dealt out evenly: CTA c of G owns [c total / G, (c + 1) total / G).
 // (total < 2^31: the blocks of 2^31 would fill more than the device's memory)
