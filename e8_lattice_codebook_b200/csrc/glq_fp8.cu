@@ -250,16 +250,16 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
             const Ahead f = a;
             if constexpr (!ROUND) fetch(i + turn, a);
             if constexpr (ROUND) {
-                uint32_t q[ROWS];
-                float s[ROWS];
-                warp_quantize_rows<T, ROWS>(f.x, p.B, q, s);
+                float inv;
+                const float s = warp_group_scales<T, ROWS>(f.x, p.B, lane, inv);
                 if (!pipe_x_begin(pipe, i, p.err)) break;
                 uint8_t *xt = pipe_x_tile<NT>(smem, i);
+                if (lane < p.B) sc[lane] = s * f.ws;
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) {
                     if (r >= p.B) break;
-                    *reinterpret_cast<uint32_t *>(xt + sw128(r, lane >> 2) + (lane & 3) * 4) = q[r];
-                    if (lane == 0) sc[r] = s[r] * f.ws;
+                    *reinterpret_cast<uint32_t *>(xt + sw128(r, lane >> 2) + (lane & 3) * 4) =
+                        round4<T>(f.x[r], __shfl_sync(0xffffffffu, inv, r));
                 }
             } else {
                 if (!pipe_x_begin(pipe, i, p.err)) break;

@@ -51,31 +51,36 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// One warp, one token, one group of 128: lane holds values 4 lane .. 4 lane
-// + 3.  Returns the packed e4m3 values and the scale.
-__device__ __forceinline__ uint32_t warp_quantize(const float v[4], float &scale) {
-    uint32_t m = max(max(mag_bits(v[0]), mag_bits(v[1])), max(mag_bits(v[2]), mag_bits(v[3])));
-    m = max(__reduce_max_sync(0xffffffffu, m), FLOOR_BITS);
-    scale = group_scale(m);
-    return e4m3x4(v, group_inv(m));
-}
-
 // Byte offset of (row, 16-byte chunk) in a K-major tile of 128-byte rows
 // with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
 
-// The same for up to ROWS rows of x, in registers: q[r] the packed values of
-// row r, scale[r] its scale.  All rows are loaded before the first is rounded.
+// One warp, a group of 128 columns of up to ROWS <= 32 tokens, whose lane l
+// holds columns 4 l .. 4 l + 3 of each (w[r], two 16-bit pairs).  The two
+// divisions are made once for all tokens, lane r having token r's: returns
+// lane r's scale, and its inverse in inv.
 template <typename T, int ROWS>
-__device__ __forceinline__ void warp_quantize_rows(const uint2 (&w)[ROWS], int live, uint32_t (&q)[ROWS],
-                                                   float (&scale)[ROWS]) {
+__device__ __forceinline__ float warp_group_scales(const uint2 (&w)[ROWS], int live, int lane, float &inv) {
+    uint32_t mine = 0;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         if (r >= live) break;
         const float2 a = unpack2<T>(w[r].x), c = unpack2<T>(w[r].y);
-        const float v[4] = {a.x, a.y, c.x, c.y};
-        q[r] = warp_quantize(v, scale[r]);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, max(max(mag_bits(a.x), mag_bits(a.y)),
+                                                              max(mag_bits(c.x), mag_bits(c.y))));
+        if (lane == r) mine = m;
     }
+    mine = max(mine, FLOOR_BITS);
+    inv = group_inv(mine);
+    return group_scale(mine);
+}
+
+// The rounded values of one such token.
+template <typename T>
+__device__ __forceinline__ uint32_t round4(uint2 w, float inv) {
+    const float2 a = unpack2<T>(w.x), c = unpack2<T>(w.y);
+    const float v[4] = {a.x, a.y, c.x, c.y};
+    return e4m3x4(v, inv);
 }
 
 // ---------------------------------------------------------------------------
