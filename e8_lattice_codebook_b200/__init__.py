@@ -44,6 +44,7 @@ EXPORTS = (
     "glq_rht_input_operand", "glq_layer_selftest_wait",
     "glq_fp8_quantize", "glq_fp8_create", "glq_fp8_destroy", "glq_fp8_reserve", "glq_fp8_linear",
     "glq_fp8_linear_quantized", "glq_fp8_dequant", "glq_fp8_check", "glq_fp8_info",
+    "glq_moe_create", "glq_moe_destroy", "glq_moe_reserve", "glq_moe_forward", "glq_moe_check", "glq_moe_info",
 )
 
 
@@ -54,6 +55,12 @@ class GlqError(RuntimeError):
 
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+
+class MoeConfig(ctypes.Structure):
+    """glq_moe_config of include/glq.h."""
+    _fields_ = [("experts", _i64), ("d", _i64), ("inter", _i64), ("topk", _i32), ("scoring", _i32),
+                ("renormalize", _i32), ("routed_scale", ctypes.c_float)]
+
 
 # argument / result types of every exported function
 _SIGNATURES = {
@@ -99,6 +106,12 @@ _SIGNATURES = {
     "glq_fp8_dequant": ([_vp, _vp, _vp], ctypes.c_int),
     "glq_fp8_check": ([_vp, _vp], ctypes.c_int),
     "glq_fp8_info": ([_vp, ctypes.POINTER(_i64), ctypes.POINTER(_i64), ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
+    "glq_moe_create": ([ctypes.POINTER(MoeConfig), _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(_vp)], ctypes.c_int),
+    "glq_moe_destroy": ([_vp], ctypes.c_int),
+    "glq_moe_reserve": ([_vp, _i64], ctypes.c_int),
+    "glq_moe_forward": ([_vp, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, ctypes.c_int, _i64, _vp], ctypes.c_int),
+    "glq_moe_check": ([_vp, _vp], ctypes.c_int),
+    "glq_moe_info": ([_vp, ctypes.POINTER(MoeConfig), ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
 }
 
 _lib = None
@@ -374,6 +387,39 @@ def glq_fp8_info(handle):
     return m.value, n.value, nb.value
 
 
+GLQ_MOE_SOFTMAX, GLQ_MOE_SIGMOID = 0, 1
+
+
+def glq_moe_create(config: MoeConfig, gate, gate_scales, up, up_scales, down, down_scales, stream) -> int:
+    h = _vp()
+    _ok(_L().glq_moe_create(ctypes.byref(config), gate, gate_scales, up, up_scales, down, down_scales, stream,
+                            ctypes.byref(h)), "glq_moe_create")
+    return h.value
+
+
+def glq_moe_destroy(handle: int) -> None:
+    _ok(_L().glq_moe_destroy(handle), "glq_moe_destroy")
+
+
+def glq_moe_reserve(handle: int, max_T: int) -> None:
+    _ok(_L().glq_moe_reserve(handle, max_T), "glq_moe_reserve")
+
+
+def glq_moe_forward(handle, x_ptr, x_dtype, logits_ptr, logits_dtype, y_ptr, y_dtype, T, stream) -> None:
+    _ok(_L().glq_moe_forward(handle, x_ptr, x_dtype, logits_ptr, logits_dtype, y_ptr, y_dtype, T, stream),
+        "glq_moe_forward")
+
+
+def glq_moe_check(handle, stream) -> None:
+    _ok(_L().glq_moe_check(handle, stream), "glq_moe_check")
+
+
+def glq_moe_info(handle):
+    c, nb = MoeConfig(), ctypes.c_size_t()
+    _ok(_L().glq_moe_info(handle, ctypes.byref(c), ctypes.byref(nb)), "glq_moe_info")
+    return {name: getattr(c, name) for name, _ in MoeConfig._fields_}, nb.value
+
+
 # ---------------------------------------------------------------------------
 # torch convenience (device memory and streams only)
 # ---------------------------------------------------------------------------
@@ -588,7 +634,7 @@ def _e4m3_matrix(name, w, device, dims=2):
         raise ValueError(f"{name} must be a float8_e4m3fn tensor of {dims} dimensions")
     w = w.to(device)
     packed = w.stride(-1) == 1 and w.stride(-2) >= w.shape[-1] and w.stride(-2) % 8 == 0 and w.data_ptr() % 8 == 0
-    return w if packed and (dims == 2 or w.is_contiguous()) else w.contiguous().clone()
+    return w if packed and (dims == 2 or w.is_contiguous()) else w.clone(memory_format=torch.contiguous_format)
 
 
 def _block_scales(name, s, device, shape):
@@ -637,12 +683,12 @@ class Fp8Linear:
         [ceil(n/128)].  Tensors of the CPU go to the current CUDA device.
         Reads them on the current stream and waits for it."""
         torch = _torch()
+        self.handle = 0
         self.device = w.device if w.is_cuda else torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
         w = _e4m3_matrix("w", w, self.device)
         self.m, self.n = int(w.shape[0]), int(w.shape[1])
         scales = _block_scales("scales", scales, self.device, (_fp8_blocks(self.m), _fp8_blocks(self.n)))
-        self.handle = 0
         with torch.cuda.device(self.device):
             self.handle = glq_fp8_create(self.m, self.n, w.data_ptr(), w.stride(0), scales.data_ptr(),
                                          _call_stream(self._index, None))
@@ -698,6 +744,73 @@ class Fp8Linear:
     def close(self):
         if self.handle:
             glq_fp8_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Fp8Moe:
+    """A mixture-of-experts layer for a few tokens, its experts e4m3 with one
+    fp32 scale per 128 x 128 block (definition: include/glq.h, "Mixture of
+    experts").  The weights are copied into the layer."""
+
+    def __init__(self, gate, gate_scales, up, up_scales, down, down_scales, topk, renormalize=True,
+                 scoring=GLQ_MOE_SOFTMAX, routed_scale=1.0):
+        """gate, up: float8_e4m3fn [E][inter][d], down: [E][d][inter] (d, inter
+        multiples of 8); scales [E][ceil(rows/128)][ceil(cols/128)].  Tensors
+        of the CPU go to the current CUDA device.  Reads them on the current
+        stream and waits for it."""
+        torch = _torch()
+        self.handle = 0
+        self.device = gate.device if gate.is_cuda else torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
+        gate, up, down = (_e4m3_matrix(n, w, self.device, 3) for n, w in (("gate", gate), ("up", up), ("down", down)))
+        self.experts, self.inter, self.d = (int(v) for v in gate.shape)
+        if tuple(up.shape) != tuple(gate.shape) or tuple(down.shape) != (self.experts, self.d, self.inter):
+            raise ValueError(f"up must be {list(gate.shape)} and down {[self.experts, self.d, self.inter]}")
+        wide, high = _fp8_blocks(self.d), _fp8_blocks(self.inter)
+        gate_scales = _block_scales("gate_scales", gate_scales, self.device, (self.experts, high, wide))
+        up_scales = _block_scales("up_scales", up_scales, self.device, (self.experts, high, wide))
+        down_scales = _block_scales("down_scales", down_scales, self.device, (self.experts, wide, high))
+        self.topk = int(topk)
+        config = MoeConfig(self.experts, self.d, self.inter, self.topk, int(scoring), int(bool(renormalize)),
+                           float(routed_scale))
+        with torch.cuda.device(self.device):
+            self.handle = glq_moe_create(config, gate.data_ptr(), gate_scales.data_ptr(), up.data_ptr(),
+                                         up_scales.data_ptr(), down.data_ptr(), down_scales.data_ptr(),
+                                         _call_stream(self._index, None))
+
+    def reserve(self, max_T: int):
+        glq_moe_reserve(self.handle, max_T)
+
+    def forward(self, x, logits, out=None, out_dtype=None, stream=None):
+        """y [T][d] of x [T][d] (fp16 or bf16) and router logits [T][E]
+        (float32 or x's dtype), in x's dtype or out_dtype (x's or float32)."""
+        _check_input("x", x, self.d, self._index)
+        _check_input("logits", logits, self.experts, self._index)
+        T = x.size(0)
+        if logits.size(0) != T:
+            raise ValueError(f"logits must have {T} rows, as x has")
+        if out is None:
+            out = x.new_empty((T, self.d), dtype=out_dtype)
+        else:
+            _check_output("out", out, (T, self.d), self._index)
+        glq_moe_forward(self.handle, x.data_ptr(), _dtype_code(x), logits.data_ptr(), _dtype_code(logits),
+                        out.data_ptr(), _dtype_code(out), T, _call_stream(self._index, stream, x, logits, out))
+        return out
+
+    __call__ = forward
+
+    def check(self, stream=None):
+        glq_moe_check(self.handle, _call_stream(self._index, stream))
+
+    def close(self):
+        if self.handle:
+            glq_moe_destroy(self.handle)
             self.handle = 0
 
     def __del__(self):

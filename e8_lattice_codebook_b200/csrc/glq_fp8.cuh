@@ -75,7 +75,16 @@ __device__ __forceinline__ float warp_group_scales(const uint2 (&w)[ROWS], int l
     return group_scale(mine);
 }
 
-// The rounded values of one such token.
+// One warp, a group of one token in fp32: lane l holds values 4 l .. 4 l + 3;
+// returns them rounded.
+__device__ __forceinline__ uint32_t warp_quantize(const float v[4], float &scale) {
+    uint32_t m = max(max(mag_bits(v[0]), mag_bits(v[1])), max(mag_bits(v[2]), mag_bits(v[3])));
+    m = max(__reduce_max_sync(0xffffffffu, m), FLOOR_BITS);
+    scale = group_scale(m);
+    return e4m3x4(v, group_inv(m));
+}
+
+// The rounded values of one token of warp_group_scales.
 template <typename T>
 __device__ __forceinline__ uint32_t round4(uint2 w, float inv) {
     const float2 a = unpack2<T>(w.x), c = unpack2<T>(w.y);

@@ -78,4 +78,36 @@ Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, const int clusters[9]);
 cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, const CUtensorMap &qmap, int source, int nt, int clusters,
                               cudaStream_t s, bool pdl);
 
+// A mixture-of-experts layer (glq_moe.cu) for T <= MOE_MAX_T tokens.  d: width
+// of x and y, inter: of an expert; KB1 = ceil(d/128) = DB, IB = ceil(inter/128).
+constexpr int MOE_MAX_T = 64, MOE_MAX_E = 512, MOE_MAX_K = 16;
+constexpr int MOE_SMEM_LIMIT = 224 * 1024;  // 227 KB less the static arrays
+struct MoeParams {
+    const void *x;       // [T][d] f16 (x_dtype 0) or bf16 (1)
+    const void *logits;  // [T][E], dtype 0 f16, 1 bf16, 2 f32
+    void *y;             // [T][d]
+    int x_dtype, logits_dtype, y_dtype;
+    int T, E, k, d;
+    int KB1, IB, DB;
+    int scoring, renormalize;  // 0 softmax, 1 sigmoid
+    float routed_scale;
+    const uint8_t *w13;  // tiles [E][2 IB][KB1]: gate and up row tiles in turn
+    const float *s13;    // [E][2 IB][KB1]
+    const uint8_t *w2;   // tiles [E][DB][IB]
+    const float *s2;     // [E][DB][IB]
+    // workspace (nt: moe_tile(T), A: experts in use)
+    uint8_t *xq;         // [KB1] operand tiles of nt x 128
+    float *xs;           // [KB1][nt]
+    float *main;         // [T k][2 IB][128]
+    float *spill;        // [grid][nt][128]
+    uint8_t *hq;         // [A][IB] operand tiles of nt x 128
+    float *hs;           // [A][IB][nt]
+    float *part;         // [grid][2][nt][128]
+    uint64_t *bar;       // grid barrier: arrivals so far, a multiple of grid between calls
+    unsigned *err;
+};
+int moe_tile(int T);
+// cooperative: `grid` CTAs, one per SM
+cudaError_t launch_moe(const MoeParams &p, int grid, cudaStream_t s);
+
 }  // namespace glq

@@ -141,6 +141,68 @@ glq_status check_word(unsigned *d_err, cudaStream_t s) {
     return (err & GLQ_DEVERR_TIMEOUT) ? GLQ_ERR_TIMEOUT : GLQ_ERR_DEVICE_CHECK;
 }
 
+// ---------------------------------------------------------------------------
+// Mixture of experts
+// ---------------------------------------------------------------------------
+
+void free_moe(glq_moe L) {
+    cudaFree(L->d_w13);
+    cudaFree(L->d_w2);
+    cudaFree(L->d_s13);
+    cudaFree(L->d_s2);
+    cudaFree(L->d_err);
+    cudaFree(L->d_bar);
+    delete L;
+}
+
+// Sets p's workspace pointers from `base` (may be null) for p.T tokens;
+// returns the bytes they span.
+size_t moe_workspace(glq_moe L, glq::MoeParams &p, uint8_t *base) {
+    const size_t nt = glq::moe_tile(p.T), slots = (size_t)p.T * p.k;
+    const size_t A = std::min<size_t>((size_t)L->experts, slots);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t *r = base ? base + off : nullptr;
+        off += (bytes + 255) & ~(size_t)255;
+        return r;
+    };
+    p.xq = take((size_t)p.KB1 * nt * 128);
+    p.xs = reinterpret_cast<float *>(take((size_t)p.KB1 * nt * 4));
+    p.main = reinterpret_cast<float *>(take(slots * 2 * p.IB * 512));
+    p.spill = reinterpret_cast<float *>(take((size_t)L->num_sms * nt * 512));
+    p.hq = take(A * p.IB * nt * 128);
+    p.hs = reinterpret_cast<float *>(take(A * p.IB * nt * 4));
+    p.part = reinterpret_cast<float *>(take((size_t)L->num_sms * 2 * nt * 512));
+    return off;
+}
+
+glq::MoeParams moe_params(glq_moe L, int T) {
+    glq::MoeParams p{};
+    p.T = T;
+    p.E = (int)L->experts;
+    p.k = L->topk;
+    p.d = (int)L->d;
+    p.KB1 = p.DB = L->DB;
+    p.IB = L->IB;
+    p.scoring = L->scoring;
+    p.renormalize = L->renormalize;
+    p.routed_scale = L->routed_scale;
+    p.w13 = L->d_w13;
+    p.s13 = L->d_s13;
+    p.w2 = L->d_w2;
+    p.s2 = L->d_s2;
+    p.bar = L->d_bar;
+    p.err = L->d_err;
+    return p;
+}
+
+void moe_need(glq_moe L, int64_t T, size_t need[glq::FP8_WS_COUNT]) {
+    for (int t : {16, 32, glq::MOE_MAX_T}) {
+        glq::MoeParams p = moe_params(L, (int)std::min<int64_t>(T, t));
+        need[glq::FP8_WS_MOE] = std::max(need[glq::FP8_WS_MOE], moe_workspace(L, p, nullptr));
+    }
+}
+
 bool good_dims(int64_t m, int64_t n) {
     return m > 0 && n > 0 && !(m & 7) && !(n & 7) && m <= GLQ_FP8_MAX_DIM && n <= GLQ_FP8_MAX_DIM;
 }
@@ -289,6 +351,156 @@ glq_status glq_fp8_info(glq_fp8 L, int64_t *m, int64_t *n, size_t *device_bytes)
     if (!L) return GLQ_ERR_INVALID_ARG;
     if (m) *m = L->m;
     if (n) *n = L->n;
+    if (device_bytes) *device_bytes = L->device_bytes;
+    return GLQ_OK;
+}
+
+glq_status glq_moe_create(const glq_moe_config *c, const void *gate_dev, const float *gate_scales_dev,
+                          const void *up_dev, const float *up_scales_dev, const void *down_dev,
+                          const float *down_scales_dev, void *stream, glq_moe *out) {
+    if (!out) return GLQ_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!c) return GLQ_ERR_INVALID_ARG;
+    if (!good_dims(c->d, c->inter) || c->experts < 1 || c->experts > glq::MOE_MAX_E || c->topk < 1 ||
+        c->topk > glq::MOE_MAX_K || c->topk > c->experts)
+        return GLQ_ERR_SHAPE;
+    // the kernel counts blocks and places in 31 bits
+    const int64_t DB = blocks_of(c->d), IB = blocks_of(c->inter);
+    if (c->experts * 2 * IB * DB > (int64_t)1 << 30) return GLQ_ERR_SHAPE;
+    if (c->scoring != GLQ_MOE_SOFTMAX && c->scoring != GLQ_MOE_SIGMOID) return GLQ_ERR_INVALID_ARG;
+    if (!(c->routed_scale - c->routed_scale == 0.f)) return GLQ_ERR_INVALID_ARG;  // not finite
+    for (const void *w : {gate_dev, up_dev, down_dev})
+        if (!w || !aligned(w, 8)) return GLQ_ERR_INVALID_ARG;
+    for (const float *s : {gate_scales_dev, up_scales_dev, down_scales_dev})
+        if (!s || !aligned(s, 4)) return GLQ_ERR_INVALID_ARG;
+    glq_moe L = new (std::nothrow) glq_moe_s;
+    if (!L) return GLQ_ERR_OOM;
+    L->experts = c->experts;
+    L->d = c->d;
+    L->inter = c->inter;
+    L->topk = c->topk;
+    L->scoring = c->scoring;
+    L->renormalize = c->renormalize ? 1 : 0;
+    L->routed_scale = c->routed_scale;
+    L->DB = (int)DB;
+    L->IB = (int)IB;
+    const int64_t tiles2 = L->experts * DB * IB, tiles13 = 2 * tiles2;
+    glq_status st = GLQ_OK;
+    if (cudaGetDevice(&L->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&L->num_sms, cudaDevAttrMultiProcessorCount, L->device) != cudaSuccess) {
+        cudaGetLastError();
+        st = GLQ_ERR_CUDA;
+    }
+    if (st == GLQ_OK) st = dev_alloc(&L->d_w13, (size_t)tiles13 * GLQ_FP8_TILE_BYTES, &L->device_bytes);
+    if (st == GLQ_OK) st = dev_alloc(&L->d_w2, (size_t)tiles2 * GLQ_FP8_TILE_BYTES, &L->device_bytes);
+    if (st == GLQ_OK) st = dev_alloc(&L->d_s13, (size_t)tiles13 * sizeof(float), &L->device_bytes);
+    if (st == GLQ_OK) st = dev_alloc(&L->d_s2, (size_t)tiles2 * sizeof(float), &L->device_bytes);
+    if (st == GLQ_OK) st = dev_alloc(&L->d_err, sizeof(unsigned), &L->device_bytes);
+    if (st == GLQ_OK) st = dev_alloc(&L->d_bar, sizeof(uint64_t), &L->device_bytes);
+    if (st == GLQ_OK) {
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        bool ok = cudaMemsetAsync(L->d_err, 0, sizeof(unsigned), s) == cudaSuccess &&
+                  cudaMemsetAsync(L->d_bar, 0, sizeof(uint64_t), s) == cudaSuccess;
+        auto pack = [&](const void *w, const float *sc, int64_t rows, int64_t cols, uint8_t *dst, float *dst_scale,
+                        int step, int off) {
+            glq::Fp8PackParams p{};
+            p.src = static_cast<const uint8_t *>(w);
+            p.src_scale = sc;
+            p.dst = dst;
+            p.dst_scale = dst_scale;
+            p.ld = cols;
+            p.rows = (int)rows;
+            p.cols = (int)cols;
+            p.KB = (int)blocks_of(cols);
+            p.rt_step = step;
+            p.rt_off = off;
+            p.count = (int)L->experts;
+            p.src_stride = rows * cols;
+            p.src_scale_stride = blocks_of(rows) * p.KB;
+            p.dst_tiles = step * blocks_of(rows) * p.KB;
+            ok = ok && glq::launch_fp8_pack(p, s) == cudaSuccess;
+        };
+        pack(gate_dev, gate_scales_dev, L->inter, L->d, L->d_w13, L->d_s13, 2, 0);
+        pack(up_dev, up_scales_dev, L->inter, L->d, L->d_w13, L->d_s13, 2, 1);
+        pack(down_dev, down_scales_dev, L->d, L->inter, L->d_w2, L->d_s2, 1, 0);
+        if (!ok || cudaStreamSynchronize(s) != cudaSuccess) {
+            cudaGetLastError();
+            st = GLQ_ERR_CUDA;
+        }
+    }
+    if (st != GLQ_OK) {
+        free_moe(L);
+        return st;
+    }
+    *out = L;
+    return GLQ_OK;
+}
+
+glq_status glq_moe_destroy(glq_moe layer) {
+    if (!layer) return GLQ_ERR_INVALID_ARG;
+    DeviceGuard guard(layer->device);
+    free_moe(layer);
+    return GLQ_OK;
+}
+
+glq_status glq_moe_reserve(glq_moe layer, int64_t max_T) {
+    if (!layer) return GLQ_ERR_INVALID_ARG;
+    if (max_T < 0) return GLQ_ERR_SHAPE;
+    if (max_T == 0) return GLQ_OK;
+    DeviceGuard guard(layer->device);
+    size_t need[glq::FP8_WS_COUNT] = {};
+    moe_need(layer, max_T, need);
+    void *buf[glq::FP8_WS_COUNT];
+    return glq::fp8_workspace(layer->device, need, 0, buf);
+}
+
+glq_status glq_moe_forward(glq_moe L, const void *x_dev, glq_dtype x_dtype, const void *logits_dev,
+                           glq_dtype logits_dtype, void *y_dev, glq_dtype y_dtype, int64_t T, void *stream) {
+    if (!L) return GLQ_ERR_INVALID_ARG;
+    if (T < 0) return GLQ_ERR_SHAPE;
+    if (x_dtype != GLQ_F16 && x_dtype != GLQ_BF16) return GLQ_ERR_DTYPE;
+    if (y_dtype != x_dtype && y_dtype != GLQ_F32) return GLQ_ERR_DTYPE;
+    if (logits_dtype != x_dtype && logits_dtype != GLQ_F32) return GLQ_ERR_DTYPE;
+    if (T == 0) return GLQ_OK;
+    if (!x_dev || !y_dev || !logits_dev || !aligned(x_dev, 16) || !aligned(y_dev, 16) ||
+        !aligned(logits_dev, logits_dtype == GLQ_F32 ? 4 : 2))
+        return GLQ_ERR_INVALID_ARG;
+    DeviceGuard guard(L->device);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    size_t need[glq::FP8_WS_COUNT] = {};
+    moe_need(L, T, need);
+    void *buf[glq::FP8_WS_COUNT];
+    const glq_status st = glq::fp8_workspace(L->device, need, s, buf);
+    if (st != GLQ_OK) return st;
+    const size_t ye = y_dtype == GLQ_F32 ? 4 : 2, le = logits_dtype == GLQ_F32 ? 4 : 2;
+    for (int64_t t = 0; t < T; t += glq::MOE_MAX_T) {
+        glq::MoeParams p = moe_params(L, (int)std::min<int64_t>(glq::MOE_MAX_T, T - t));
+        p.x = static_cast<const char *>(x_dev) + (size_t)t * L->d * 2;
+        p.logits = static_cast<const char *>(logits_dev) + (size_t)t * L->experts * le;
+        p.y = static_cast<char *>(y_dev) + (size_t)t * L->d * ye;
+        p.x_dtype = (int)x_dtype;
+        p.logits_dtype = (int)logits_dtype;
+        p.y_dtype = (int)y_dtype;
+        moe_workspace(L, p, static_cast<uint8_t *>(buf[glq::FP8_WS_MOE]));
+        const glq_status e = launched(glq::launch_moe(p, L->num_sms, s));
+        if (e != GLQ_OK) return e;
+    }
+    return GLQ_OK;
+}
+
+glq_status glq_moe_check(glq_moe L, void *stream) {
+    if (!L) return GLQ_ERR_INVALID_ARG;
+    DeviceGuard guard(L->device);
+    const glq_status st = check_word(L->d_err, static_cast<cudaStream_t>(stream));
+    // a call that gave up may have left the grid barrier half way
+    if (st == GLQ_ERR_TIMEOUT) cudaMemset(L->d_bar, 0, sizeof(uint64_t));
+    return st;
+}
+
+glq_status glq_moe_info(glq_moe L, glq_moe_config *config, size_t *device_bytes) {
+    if (!L) return GLQ_ERR_INVALID_ARG;
+    if (config)
+        *config = glq_moe_config{L->experts, L->d, L->inter, L->topk, L->scoring, L->renormalize, L->routed_scale};
     if (device_bytes) *device_bytes = L->device_bytes;
     return GLQ_OK;
 }

@@ -114,6 +114,20 @@ struct glq_fp8_s {
     size_t device_bytes = 0;
 };
 
+// A mixture-of-experts layer with e4m3 experts.
+struct glq_moe_s {
+    int64_t experts = 0, d = 0, inter = 0;
+    int topk = 0, scoring = 0, renormalize = 0;
+    float routed_scale = 1.f;
+    int DB = 0, IB = 0;           // 128-blocks of d and inter
+    int device = 0, num_sms = 0;
+    uint8_t *d_w13 = nullptr, *d_w2 = nullptr;  // operand tiles (glq_fp8.h)
+    float *d_s13 = nullptr, *d_s2 = nullptr;
+    unsigned *d_err = nullptr;
+    uint64_t *d_bar = nullptr;    // grid barrier
+    size_t device_bytes = 0;
+};
+
 namespace glq {
 
 // Makes `dev` the current device while it lives.
@@ -131,8 +145,8 @@ struct DeviceGuard {
 };
 
 // The 8-bit float operators' buffers in the device's shared workspace:
-// rounded activations and their scales.
-enum Fp8Ws { FP8_WS_Q, FP8_WS_S, FP8_WS_COUNT };
+// rounded activations, their scales, all of a mixture-of-experts call.
+enum Fp8Ws { FP8_WS_Q, FP8_WS_S, FP8_WS_MOE, FP8_WS_COUNT };
 // Makes each at least need[i] bytes (the rules of the shared workspace hold:
 // growth synchronises, and is refused during stream capture).
 glq_status fp8_workspace(int dev, const size_t need[FP8_WS_COUNT], cudaStream_t s, void *out[FP8_WS_COUNT]);

@@ -1,0 +1,488 @@
+// glq_moe.cu -- a mixture-of-experts layer for a few tokens in one kernel.
+//
+//     y[t] = sum over t's experts e of  p[t][e] down_e h^_e(t),
+//     h_e(t) = silu(gate_e x^(t)) * (up_e x^(t)),
+//
+// x^ and h^ the e4m3 roundings of x and h (a scale per token and 128 columns),
+// the matrices e4m3 with a scale per 128 x 128 block, p the softmax (or
+// sigmoid) of the token's chosen router logits.
+//
+// Bound by HBM: the weights of every chosen expert are read once, 16 KB tile
+// by tile (glq_fp8.h), by the few-token pipeline of glq_fp8.cuh, whose MMA
+// takes all tokens as its N side whichever expert the tile belongs to (the
+// tensor cores have time to spare; a token that did not choose the expert is
+// dropped when the result is read).  The tiles of a phase form one sequence,
+// dealt out evenly over the CTAs, one per SM, so that an odd number of experts
+// or rows leaves no SM idle; a tile that falls to two or more CTAs is summed
+// by whoever reads it, in the order of the CTAs.  Phases, with a barrier over
+// the grid (a cooperative launch) after each:
+//   0  every CTA: the routing of all tokens, for itself; a share of x^
+//   1  gate and up tiles -> fp32 sums per (token, expert)
+//   h  silu, product, rounding -> h^ as operand tiles
+//   2  down tiles -> sums per token over experts; whole tiles go to y
+//   y  the tiles of y that were split
+// The copy warp runs ahead across the barriers: while a CTA waits, its first
+// stages of the next phase's weights (up to 11 x 16 KB) are on their way.
+#include "glq_fp8.cuh"
+#include "glq_kernels.cuh"
+
+namespace glq {
+
+namespace {
+
+using namespace fp8;
+
+constexpr int WARPS = D_WARP0 + D_WARPS + 1;  // the pipeline's and one that keeps the grid's barriers
+constexpr int THREADS = WARPS * 32;           // 608
+constexpr int GRID_WARP = WARPS - 1;
+constexpr int H_WARPS = X_WARPS + D_WARPS;    // warps that form h^
+constexpr uint8_t NONE = 0xFF;
+
+// Shared memory behind the stages.
+struct Layout {
+    uint32_t mask, wts, rank, list, ids, slot, end;
+};
+__host__ __device__ inline Layout layout_of(uint32_t base, int nt, int T, int E, int k) {
+    const int most = E < T * k ? E : T * k;  // experts in use, at most
+    Layout l;
+    l.mask = base;                                  // [E] 64-bit: tokens that chose the expert
+    l.wts = l.mask + (uint32_t)E * 8;               // [T][k] fp32: p
+    l.rank = l.wts + (uint32_t)(T * k) * 4;         // [E] 16-bit: place among the experts in use
+    l.list = l.rank + (uint32_t)E * 2;              // [most] 16-bit: experts in use
+    l.ids = l.list + (uint32_t)most * 2;            // [T][k] 16-bit: chosen experts, -1 none
+    l.slot = (l.ids + (uint32_t)(T * k) * 2 + 15) & ~15u;  // [most][nt]: which of t's choices, or NONE
+    l.end = l.slot + (uint32_t)most * nt;
+    return l;
+}
+
+// Monotonic key of a logit: larger for larger values, 0 for those never chosen
+// (NaN, -inf); -0 counts as 0.
+__device__ __forceinline__ uint32_t logit_key(float v) {
+    if (!(v > -INFINITY)) return 0;
+    const uint32_t b = __float_as_uint(v + 0.f);
+    return (b >> 31) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+    return __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
+}
+
+__device__ __forceinline__ float load_logit(const MoeParams &p, int64_t i) {
+    if (p.logits_dtype == 2) return __ldg(static_cast<const float *>(p.logits) + i);
+    if (p.logits_dtype == 1) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[i]);
+    return __half2float(static_cast<const __half *>(p.logits)[i]);
+}
+
+// One warp: the k largest logits of token t, ties to the lowest index, and
+// their weights.  Lane l has experts l, l + 32, ... (NV of them).
+template <int NV>
+__device__ __forceinline__ void route(const MoeParams &p, int t, int lane, int16_t *ids, float *wts,
+                                      unsigned long long *mask) {
+    uint32_t key[NV];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = e < p.E ? logit_key(load_logit(p, (int64_t)t * p.E + e)) : 0;
+    }
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+    const float top = key_logit(__reduce_max_sync(0xffffffffu, best));
+    if (!p.renormalize && p.scoring == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (key[i]) sum += expf(key_logit(key[i]) - top);
+        sum = warp_sum(sum);
+    }
+    float mine = 0.f;  // lane j: the weight of choice j
+    for (int j = 0; j < p.k; ++j) {
+        best = 0;
+        uint32_t at = 0;
+#pragma unroll
+        for (int i = NV - 1; i >= 0; --i)  // downwards: the lowest index of equals stays
+            if (key[i] >= best) best = key[i], at = i * 32 + lane;
+        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, best == m ? at : 0xFFFFFFFFu);
+        if (m == 0) {  // nothing left to choose
+            if (lane == 0) ids[j] = -1;
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((uint32_t)(i * 32 + lane) == e) key[i] = 0;
+        const float l = key_logit(m);
+        const float w = p.scoring == 0 ? expf(l - top) : 1.f / (1.f + expf(-l));
+        if (p.renormalize) sum += w;
+        if (lane == j) mine = w;
+        if (lane == 0) {
+            ids[j] = (int16_t)e;
+            atomicOr(mask + e, 1ull << t);
+        }
+    }
+    if (p.renormalize || p.scoring == 0) mine = mine / sum;
+    if (lane < p.k) wts[lane] = mine * p.routed_scale;
+}
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ uint64_t atom_add_u64(uint64_t *p, uint64_t v) {
+    uint64_t old;
+    asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(old) : "l"(p), "l"(v) : "memory");
+    return old;
+}
+__device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t *p) {
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+__device__ __forceinline__ float silu(float v) { return v / (1.f + expf(-v)); }
+
+template <int NT>
+__global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
+    using P = Pipe<NT>;
+    constexpr int HALF = NT / 2, STAGES = P::STAGES, DRAIN = P::DRAIN;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(16) P pipe;
+    // grid[n]: the grid's barrier n has been passed.  part1, formed, part2:
+    // this CTA's warps have written their share of the phase.
+    __shared__ uint64_t grid_bar[4], part1, formed, part2;
+    __shared__ int s_count;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = blockIdx.x, G = gridDim.x;
+    const int T = p.T, E = p.E, K = p.k;
+    const Layout at = layout_of(STAGES * P::STAGE_BYTES, NT, T, E, K);
+    unsigned long long *mask = reinterpret_cast<unsigned long long *>(smem + at.mask);
+    float *wts = reinterpret_cast<float *>(smem + at.wts);
+    int16_t *rank = reinterpret_cast<int16_t *>(smem + at.rank), *list = reinterpret_cast<int16_t *>(smem + at.list);
+    int16_t *ids = reinterpret_cast<int16_t *>(smem + at.ids);
+    uint8_t *slot = smem + at.slot;
+
+    // ---------------- phase 0: setup, x^, routing ----------------
+    if (warp == 0) {
+        pipe.init(lane, 1);
+        if (lane == 0) {
+            for (int i = 0; i < 4; ++i) mbar_init(&grid_bar[i], 1);
+            mbar_init(&part1, D_WARPS);
+            mbar_init(&formed, H_WARPS);
+            mbar_init(&part2, D_WARPS);
+        }
+    }
+    if (warp == 1) {
+        sm100::tmem_alloc(&pipe.tmem, P::TMEM_COLS);
+        sm100::tmem_relinquish();
+    }
+    for (int e = tid; e < E; e += THREADS) mask[e] = 0;
+    for (int i = tid; i < (int)(at.end - at.slot) / 4; i += THREADS) reinterpret_cast<uint32_t *>(slot)[i] = 0xFFFFFFFFu;
+    // this CTA's share of x^: a warp per token and group
+    for (int i = warp * G + cta; i < T * p.KB1; i += WARPS * G) {
+        const int t = i / p.KB1, kb = i - t * p.KB1, col = kb * GLQ_FP8_BLOCK + lane * 4;
+        uint2 w = make_uint2(0, 0);  // d is a multiple of 8: a lane's four columns are in or out together
+        if (col < p.d) w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.d + col));
+        const float2 a = p.x_dtype ? unpack2<__nv_bfloat16>(w.x) : unpack2<__half>(w.x);
+        const float2 b = p.x_dtype ? unpack2<__nv_bfloat16>(w.y) : unpack2<__half>(w.y);
+        const float v[4] = {a.x, a.y, b.x, b.y};
+        float s;
+        const uint32_t q = warp_quantize(v, s);
+        __stcg(reinterpret_cast<uint32_t *>(p.xq + (int64_t)kb * (NT * 128) + sw128(t, lane >> 2)) + (lane & 3), q);
+        if (lane == 0) __stcg(p.xs + kb * NT + t, s);
+    }
+    fence_proxy_async();  // x^ is read by bulk copies
+    __syncthreads();
+    for (int t = warp; t < T; t += WARPS) {
+        if (E <= 128) route<4>(p, t, lane, ids + t * K, wts + t * K, mask);
+        else route<16>(p, t, lane, ids + t * K, wts + t * K, mask);
+    }
+    sm100::tc_fence_before();
+    __syncthreads();
+    sm100::tc_fence_after();
+    if (warp == 0) {  // experts in use, in order
+        int n = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const bool used = e0 + lane < E && mask[e0 + lane] != 0;
+            const unsigned b = __ballot_sync(0xffffffffu, used);
+            if (used) {
+                const int r = n + __popc(b & ((1u << lane) - 1));
+                rank[e0 + lane] = (int16_t)r;
+                list[r] = (int16_t)(e0 + lane);
+            }
+            n += __popc(b);
+        }
+        if (lane == 0) s_count = n;
+    }
+    __syncthreads();
+    for (int i = tid; i < T * K; i += THREADS)
+        if (ids[i] >= 0) slot[rank[ids[i]] * NT + i / K] = (uint8_t)(i % K);
+    __syncthreads();
+
+    const uint32_t A = s_count, R1 = 2 * p.IB, KB1 = p.KB1, IB = p.IB, DB = p.DB, K2 = A * IB;
+    const uint32_t total1 = A * R1 * KB1, total2 = DB * K2;
+    // CTAs that take part in each phase: as many as there are blocks, so that
+    // none between the first and the last of a tile is without one
+    const uint32_t G1 = min((uint32_t)G, total1), G2 = min((uint32_t)G, total2);
+    const uint32_t b1 = cta < (int)G1 ? range_begin(cta, total1, G1) : 0;
+    const uint32_t n1 = cta < (int)G1 ? range_begin(cta + 1, total1, G1) - b1 : 0;
+    const uint32_t b2 = cta < (int)G2 ? range_begin(cta, total2, G2) : 0;
+    const uint32_t n2 = cta < (int)G2 ? range_begin(cta + 1, total2, G2) - b2 : 0;
+    uint32_t it = 0;  // the copy thread: blocks whose copies have been started
+    bool copier = false;
+
+    if (A == 0) {  // no token has an expert (the same in every CTA)
+        for (int64_t i = (int64_t)cta * THREADS + tid; i < (int64_t)T * p.d; i += (int64_t)G * THREADS)
+            store_y(p.y, p.y_dtype, i, 0.f);
+    } else if (warp == 0) {
+        if (elect_one()) {
+            copier = true;
+            Loader<NT> ld(smem);
+            // one phase: the blocks [b, b + n), whose weight tiles are w(b) and
+            // token tiles x(b); the token tiles exist once `bar` completes
+            auto phase = [&](uint32_t b, uint32_t n, uint64_t *bar, auto w, auto x) {
+                const uint32_t ahead = min(n, (uint32_t)STAGES);
+                Loader<NT> lx = ld;
+                for (uint32_t i = 0; i < ahead; ++i, ++it, ld.next())
+                    if (!pipe_load<NT, false>(pipe, ld, w(b + i), NT * 128, p.err)) return false;
+                if (!pipe.wait(bar, 0, p.err)) return false;
+                fence_proxy_async();
+                for (uint32_t i = 0; i < n; ++i) {
+                    if (i >= ahead) {
+                        if (!pipe_load<NT, false>(pipe, ld, w(b + i), NT * 128, p.err)) return false;
+                        ++it;
+                        ld.next();
+                    }
+                    bulk_g2s(lx.dst + GLQ_FP8_TILE_BYTES, x(b + i), NT * 128, &pipe.full[lx.stage]);
+                    lx.next();
+                }
+                return true;
+            };
+            const bool ok = phase(
+                b1, n1, &grid_bar[0],
+                [&](uint32_t b) {
+                    const uint32_t a = b / (R1 * KB1);
+                    return p.w13 + ((int64_t)list[a] * (R1 * KB1) + (b - a * (R1 * KB1))) * GLQ_FP8_TILE_BYTES;
+                },
+                [&](uint32_t b) { return p.xq + (int64_t)(b % KB1) * (NT * 128); });
+            if (ok)
+                phase(
+                    b2, n2, &grid_bar[2],
+                    [&](uint32_t b) {
+                        const uint32_t rt = b / K2, k = b - rt * K2, a = k / IB;
+                        return p.w2 + (((int64_t)list[a] * DB + rt) * IB + (k - a * IB)) * GLQ_FP8_TILE_BYTES;
+                    },
+                    [&](uint32_t b) { return p.hq + (int64_t)(b % K2) * (NT * 128); });
+        }
+    } else if (warp == 1) {
+        if (elect_one()) {
+            pipe_mma<NT>(pipe, smem, 0, n1 + n2, p.err);
+            sm100::mma_commit(&pipe.mma_done);  // every MMA issued has completed
+            sm100::mbar_wait(&pipe.mma_done, 0, WAIT_CYCLES);
+        }
+    } else if (warp == GRID_WARP) {
+        if (lane == 0) {
+            uint64_t *const mine[4] = {nullptr, &part1, &formed, &part2};
+            for (int n = 0; n < 4; ++n) {
+                if (mine[n] && !pipe.wait(mine[n], 0, p.err)) break;
+                // release: what this CTA's warps wrote before they arrived
+                const uint64_t old = atom_add_u64(p.bar, 1);
+                const uint64_t target = (old / G + 1) * G;  // every call adds 4 G
+                const uint64_t t0 = sm100::clock_cycles();
+                bool ok = true;
+                while (ok && ld_acquire_u64(p.bar) < target) {
+                    if (pipe.abort) ok = false;
+                    else if (sm100::clock_cycles() - t0 > WAIT_CYCLES) pipe.fail(p.err), ok = false;
+                }
+                if (!ok) break;
+                sm100::mbar_arrive(&grid_bar[n]);
+            }
+        }
+    } else {
+        // h^: a warp per (token, choice) and group of the expert's width
+        auto form = [&]() {
+            if (!pipe.wait_warp(&grid_bar[1], 0, p.err)) return false;
+            for (int i = (warp - X_WARP0) * G + cta; i < T * K * (int)IB; i += H_WARPS * G) {
+                const int s = i / (int)IB, ib = i - s * (int)IB, e = ids[s], t = s / K;
+                if (e < 0) continue;
+                const uint32_t a = rank[e];
+                float4 v[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // gate, up
+                    const uint32_t r = 2 * ib + h, first = (a * R1 + r) * KB1;
+                    const int c0 = range_owner(first, total1, G1), c1 = range_owner(first + KB1 - 1, total1, G1);
+                    v[h] = __ldcg(reinterpret_cast<const float4 *>(p.main + ((int64_t)s * R1 + r) * 128 + lane * 4));
+                    for (int c = c0 + 1; c <= c1; ++c)
+                        v[h] = add4(v[h], __ldcg(reinterpret_cast<const float4 *>(p.spill + ((int64_t)c * NT + t) * 128 + lane * 4)));
+                }
+                const float h[4] = {silu(v[0].x) * v[1].x, silu(v[0].y) * v[1].y, silu(v[0].z) * v[1].z,
+                                    silu(v[0].w) * v[1].w};
+                float sc;
+                const uint32_t q = warp_quantize(h, sc);
+                const int64_t tile = (int64_t)a * IB + ib;
+                __stcg(reinterpret_cast<uint32_t *>(p.hq + tile * (NT * 128) + sw128(t, lane >> 2)) + (lane & 3), q);
+                if (lane == 0) __stcg(p.hs + tile * NT + t, sc * wts[s]);
+            }
+            fence_proxy_async();  // h^ is read by bulk copies
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&formed);
+            return true;
+        };
+        if (warp < D_WARP0) {
+            // ---------------- scales ----------------
+            constexpr int SC = (NT + 31) / 32;
+            const uint32_t turn = P::X_TURN, w0 = warp - X_WARP0;
+            auto put = [&](uint32_t i, const float (&s)[SC]) {
+                if (!pipe_x_begin(pipe, i, p.err)) return false;
+#pragma unroll
+                for (int j = 0; j < SC; ++j)
+                    if (j * 32 + lane < NT) pipe.sc[i % STAGES][j * 32 + lane] = s[j];
+                pipe_x_done<NT, false>(pipe, i, lane);
+                return true;
+            };
+            bool ok = pipe.wait_warp(&grid_bar[0], 0, p.err);
+            uint32_t i = w0;
+            if (w0 >= turn) i = n1 + n2;
+            for (; ok && i < n1; i += turn) {
+                const uint32_t b = b1 + i, a = b / (R1 * KB1), kb = b % KB1;
+                const float ws = __ldg(p.s13 + (int64_t)list[a] * (R1 * KB1) + (b - a * (R1 * KB1)));
+                float s[SC];
+#pragma unroll
+                for (int j = 0; j < SC; ++j) s[j] = j * 32 + lane < T ? __ldcg(p.xs + kb * NT + j * 32 + lane) * ws : 0.f;
+                ok = put(i, s);
+            }
+            ok = ok && form() && pipe.wait_warp(&grid_bar[2], 0, p.err);
+            for (; ok && i < n1 + n2; i += turn) {
+                const uint32_t b = b2 + (i - n1), rt = b / K2, k = b - rt * K2, a = k / IB;
+                const float ws = __ldg(p.s2 + ((int64_t)list[a] * DB + rt) * IB + (k - a * IB));
+                float s[SC];
+#pragma unroll
+                for (int j = 0; j < SC; ++j) {
+                    const int t = j * 32 + lane;
+                    s[j] = t < T && slot[a * NT + t] != NONE ? __ldcg(p.hs + (int64_t)k * NT + t) * ws : 0.f;
+                }
+                ok = put(i, s);
+            }
+        } else {
+            // ---------------- drain ----------------
+            const int quadrant = warp & 3, set = (warp - D_WARP0) >> 2;
+            const int row = 32 * quadrant + lane, dtid = tid - D_WARP0 * 32;
+            float acc[HALF];
+            uint32_t i = 0;
+            bool ok = true;
+            // phase 1: sums per (token, expert); the piece with a tile's first
+            // block in `main`, a CTA's piece of an earlier CTA's tile in `spill`
+            uint32_t tile = b1 / KB1, kb = b1 - tile * KB1;
+            while (ok && i < n1) {
+                const uint32_t len = min(KB1 - kb, n1 - i);
+#pragma unroll
+                for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
+                for (uint32_t n = 0; ok && n < len;) {
+                    const bool two = DRAIN == 2 && n + 2 <= len;
+                    ok = two ? pipe_drain<NT, DRAIN, false>(pipe, i, quadrant, set, acc, p.err)
+                             : pipe_drain<NT, 1, false>(pipe, i, quadrant, set, acc, p.err);
+                    n += two ? 2 : 1;
+                    i += two ? 2 : 1;
+                }
+                if (!ok) break;
+                const uint32_t a = tile / R1, r = tile - a * R1;
+#pragma unroll
+                for (int j = 0; j < HALF; ++j) {
+                    const int t = set * HALF + j;
+                    const uint8_t c = slot[a * NT + t];
+                    if (c == NONE) continue;
+                    __stcg(kb == 0 ? p.main + (((int64_t)t * K + c) * R1 + r) * 128 + row
+                                   : p.spill + ((int64_t)cta * NT + t) * 128 + row, acc[j]);
+                }
+                ++tile;
+                kb = 0;
+            }
+            __syncwarp();
+            if (ok && lane == 0) sm100::mbar_arrive(&part1);
+            ok = ok && form();
+            // phase 2
+            tile = b2 / K2;
+            uint32_t k = b2 - tile * K2;
+            while (ok && i < n1 + n2) {
+                const uint32_t len = min(K2 - k, n1 + n2 - i);
+#pragma unroll
+                for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
+                for (uint32_t n = 0; ok && n < len;) {
+                    const bool two = DRAIN == 2 && n + 2 <= len;
+                    ok = two ? pipe_drain<NT, DRAIN, true>(pipe, i, quadrant, set, acc, p.err)
+                             : pipe_drain<NT, 1, true>(pipe, i, quadrant, set, acc, p.err);
+                    n += two ? 2 : 1;
+                    i += two ? 2 : 1;
+                }
+                if (!ok) break;
+                const bool whole = k == 0 && len == K2;
+                const int64_t col = (int64_t)tile * 128 + row;
+                float *part = p.part + ((int64_t)cta * 2 + (k == 0 ? 1 : 0)) * NT * 128 + row;
+#pragma unroll
+                for (int j = 0; j < HALF; ++j) {
+                    const int t = set * HALF + j;
+                    if (t >= T) continue;
+                    if (!whole) __stcg(part + t * 128, acc[j]);
+                    else if (col < p.d) store_y(p.y, p.y_dtype, (int64_t)t * p.d + col, acc[j]);
+                }
+                ++tile;
+                k = 0;
+            }
+            __syncwarp();
+            if (ok && lane == 0) sm100::mbar_arrive(&part2);
+            ok = ok && pipe.wait_warp(&grid_bar[3], 0, p.err);
+            // the tiles that were split: four columns of one token per thread
+            for (int j = cta * (D_WARPS * 32) + dtid; ok && j < T * (int)DB * 32; j += G * D_WARPS * 32) {
+                const int t = j / ((int)DB * 32), c4 = j - t * ((int)DB * 32), rt = c4 >> 5, col = c4 * 4;
+                const uint32_t first = rt * K2;
+                const int c0 = range_owner(first, total2, G2), c1 = range_owner(first + K2 - 1, total2, G2);
+                if (c0 == c1 || col >= p.d) continue;
+                const int64_t off = (int64_t)t * 128 + (c4 & 31) * 4;
+                float4 sum = __ldcg(reinterpret_cast<const float4 *>(p.part + ((int64_t)c0 * 2 + 1) * NT * 128 + off));
+#pragma unroll 4
+                for (int c = c0 + 1; c <= c1; ++c)
+                    sum = add4(sum, __ldcg(reinterpret_cast<const float4 *>(p.part + (int64_t)c * 2 * NT * 128 + off)));
+                store_y4(p.y, p.y_dtype, (int64_t)t * p.d + col, sum);
+            }
+        }
+    }
+    sm100::tc_fence_before();
+    __syncthreads();
+    if (copier && pipe.abort) pipe_load_drain(pipe, it);
+    __syncwarp();
+    if (warp == 1) {
+        sm100::tc_fence_after();
+        sm100::tmem_dealloc(pipe.tmem, P::TMEM_COLS);
+    }
+}
+
+struct MoeKernel {
+    const void *fn;
+    size_t smem;
+    int key;
+};
+
+template <int NT>
+MoeKernel moe_kernel_of(const MoeParams &p, int key) {
+    return {(const void *)moe_kernel<NT>,
+            1024 + layout_of(Pipe<NT>::STAGES * Pipe<NT>::STAGE_BYTES, NT, p.T, p.E, p.k).end, key};
+}
+
+}  // namespace
+
+int moe_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+
+cudaError_t launch_moe(const MoeParams &p, int grid, cudaStream_t s) {
+    const int nt = moe_tile(p.T);
+    const MoeKernel k = nt == 16 ? moe_kernel_of<16>(p, 0) : nt == 32 ? moe_kernel_of<32>(p, 1) : moe_kernel_of<64>(p, 2);
+    static std::atomic<uint64_t> configured[3];
+    const cudaError_t e = once_per_device(configured[k.key], [&k] {
+        return cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, MOE_SMEM_LIMIT);
+    });
+    if (e != cudaSuccess) return e;
+    if (k.smem > MOE_SMEM_LIMIT) return cudaErrorInvalidValue;
+    MoeParams q = p;
+    void *args[] = {&q};
+    return cudaLaunchCooperativeKernel(k.fn, dim3(grid), dim3(THREADS), args, k.smem, s);
+}
+
+}  // namespace glq

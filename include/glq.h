@@ -77,6 +77,7 @@ typedef enum { GLQ_F16 = 0, GLQ_BF16 = 1, GLQ_F32 = 2 } glq_dtype;
 typedef struct glq_codebook_s *glq_codebook;
 typedef struct glq_layer_s *glq_layer;
 typedef struct glq_fp8_s *glq_fp8;
+typedef struct glq_moe_s *glq_moe;
 
 /* Human-readable name of a status.  Never NULL; static storage. */
 GLQ_API const char *glq_status_str(glq_status s);
@@ -550,6 +551,71 @@ GLQ_API glq_status glq_fp8_check(glq_fp8 layer, void *stream);
 
 /* Layer geometry.  Any output may be NULL. */
 GLQ_API glq_status glq_fp8_info(glq_fp8 layer, int64_t *m, int64_t *n, size_t *device_bytes);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Mixture of experts: experts that are 8-bit float layers, for the few tokens
+ * of a decode step, in one kernel.  For token t with router logits l[t][0..E):
+ *     its experts are the topk largest logits (equal ones: the lowest index);
+ *     an expert whose logit is -infinity or NaN is never chosen, so a token
+ *     may have fewer, or none (then y[t] = 0);
+ *     p_e = softmax of l[t] over all experts (GLQ_MOE_SOFTMAX; those never
+ *     chosen count 0) or 1 / (1 + exp(-l)) (GLQ_MOE_SIGMOID), divided by its
+ *     sum over the chosen experts if renormalize is set, times routed_scale;
+ *     h_e = silu(gate_e x) * (up_e x), y[t] = sum_e p_e down_e h_e,
+ * where x and each h_e are rounded as glq_fp8_quantize does and each product
+ * is that of an 8-bit float layer.  Sums are fp32, y is rounded once.  A
+ * logit of +infinity gives its token NaN.  The order in which a token's sums
+ * are added depends on the other tokens of the call.  (No counterpart in the
+ * GLQ pages.)
+ * ---------------------------------------------------------------------------
+ */
+#define GLQ_MOE_SOFTMAX 0
+#define GLQ_MOE_SIGMOID 1
+typedef struct {
+    int64_t experts, d, inter; /* experts <= 512; width of x and y; of an expert */
+    int32_t topk;              /* 1 .. 16, at most experts */
+    int32_t scoring;           /* GLQ_MOE_SOFTMAX or GLQ_MOE_SIGMOID */
+    int32_t renormalize;       /* 0 or 1 */
+    float routed_scale;        /* finite */
+} glq_moe_config;
+
+/*
+ * glq_moe_create -- build the layer on the current device.
+ * gate_dev, up_dev: device e4m3 [experts][inter][d], down_dev: [experts][d]
+ *   [inter], contiguous, 8-byte aligned; the scales fp32 per expert, gate and
+ *   up [ceil(inter/128)][ceil(d/128)], down [ceil(d/128)][ceil(inter/128)].
+ *   d and inter positive multiples of 8.  Read on `stream` and copied.
+ * Errors as glq_fp8_create.  Synchronises `stream`.
+ */
+GLQ_API glq_status glq_moe_create(const glq_moe_config *config, const void *gate_dev, const float *gate_scales_dev,
+                                  const void *up_dev, const float *up_scales_dev, const void *down_dev,
+                                  const float *down_scales_dev, void *stream, glq_moe *out);
+GLQ_API glq_status glq_moe_destroy(glq_moe layer);
+
+/*
+ * glq_moe_reserve -- glq_layer_reserve for this layer: afterwards calls with
+ * T <= max_T allocate nothing and may be captured in a CUDA graph.
+ */
+GLQ_API glq_status glq_moe_reserve(glq_moe layer, int64_t max_T);
+
+/*
+ * glq_moe_forward -- y_dev [T][d] (x's dtype or GLQ_F32) of x_dev [T][d]
+ * (GLQ_F16 or GLQ_BF16) and logits_dev [T][experts] (GLQ_F32 or x's dtype);
+ * device, row-major, x and y 16-byte aligned.  T >= 0; more than 64 tokens
+ * run 64 at a time, the weights read once for each 64.  One kernel per 64
+ * tokens, a cooperative launch of one CTA per SM: it starts when every SM is
+ * free.  Workspace and serialisation as glq_linear.  Errors as glq_linear.
+ * Asynchronous.
+ */
+GLQ_API glq_status glq_moe_forward(glq_moe layer, const void *x_dev, glq_dtype x_dtype, const void *logits_dev,
+                                   glq_dtype logits_dtype, void *y_dev, glq_dtype y_dtype, int64_t T, void *stream);
+
+/* glq_moe_check -- glq_layer_check for this layer. */
+GLQ_API glq_status glq_moe_check(glq_moe layer, void *stream);
+
+/* Layer geometry.  Any output may be NULL. */
+GLQ_API glq_status glq_moe_info(glq_moe layer, glq_moe_config *config, size_t *device_bytes);
 
 #ifdef __cplusplus
 }

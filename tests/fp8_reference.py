@@ -76,3 +76,68 @@ def linear_bound(xv, wv, ref, dtype):
     n = xv.shape[1]
     terms = min(n, G) + 4 * (-(-n // G)) + 4
     return half_step(dtype) * np.abs(ref) + terms * 2.0 ** -23 * mag + smallest(dtype)
+
+
+# ---------------------------------------------------------------------------
+# Mixture of experts
+# ---------------------------------------------------------------------------
+
+def route(logits: np.ndarray, topk: int, renormalize: bool, scoring: int, scale: float):
+    """[(expert, weight), ...] per token: the largest logits, the lowest index
+    first among equals, never -inf or NaN."""
+    out = []
+    for row in logits:
+        ok = [e for e in range(len(row)) if row[e] > -np.inf]
+        best = sorted(ok, key=lambda e: (-row[e], e))[:topk]
+        if scoring == 0:
+            top = max((row[e] for e in ok), default=0.0)
+            w = {e: np.exp(row[e] - top) for e in ok}
+            total = sum(w[e] for e in (best if renormalize else ok))
+        else:
+            w = {e: 1.0 / (1.0 + np.exp(-row[e])) for e in best}
+            total = sum(w[e] for e in best) if renormalize else 1.0
+        out.append([(e, w[e] / total * scale) for e in best])
+    return out
+
+
+def _between(h, err):
+    """How far the values held for h may be apart when h itself is known to
+    +-err: (held values, bound).  A value near the middle of two e4m3 values
+    may fall to either."""
+    n = h.shape[1]
+    q, s = quantize(h.astype(np.float32).astype(np.float64))
+    held = (q * np.repeat(s.T, G, axis=1))[:, :n]
+    bound = np.zeros_like(held)
+    for g in range(0, n, G):
+        v, e = np.abs(h[:, g:g + G]), err[:, g:g + G]
+        a = np.maximum(v.max(axis=1, keepdims=True), FLOOR)
+        rel = np.max(e, axis=1, keepdims=True) / a + 2.0 ** -22  # of the scale
+        z = v * TOP / a
+        dz = e * TOP / a + z * rel
+        lo, hi = e4m3_round(np.maximum(z - dz, 0)), e4m3_round(z + dz)
+        bound[:, g:g + G] = (np.abs(hi - lo) + hi * rel) * a / TOP
+    return held, bound
+
+
+def moe(x, logits, gate, up, down, topk, renormalize, scoring, scale):
+    """(y, bound): the layer in 64 bits and how far fp32 arithmetic may be from
+    it before y's own rounding.  gate, up, down: lists of weight values."""
+    xv = values(x)
+    y, bound = np.zeros_like(x), np.zeros_like(x)
+    n_x, n_h = x.shape[1], gate[0].shape[0]
+    terms = lambda n: (min(n, G) + 4 * (-(-n // G)) + 8) * 2.0 ** -23  # noqa: E731  (as linear_bound, split sums)
+    for t, chosen in enumerate(route(logits, topk, renormalize, scoring, scale)):
+        for e, p in chosen:
+            v = xv[t:t + 1]
+            g, u = v @ gate[e].T, v @ up[e].T
+            eg, eu = (terms(n_x) * (np.abs(v) @ np.abs(w[e]).T) for w in (gate, up))
+            sig = 1.0 / (1.0 + np.exp(-g))
+            h = g * sig * u
+            # |silu'| <= 1.1; exp, sum, quotient and product lose a few units each
+            eh = 1.1 * eg * np.abs(u) + np.abs(g * sig) * eu + 1.1 * eg * eu + np.abs(h) * (np.abs(g) + 16) * 2.0 ** -23
+            held, b = _between(h, eh)
+            y[t] += p * (held @ down[e].T)[0]
+            mag = np.abs(held) @ np.abs(down[e]).T
+            ep = (logits.shape[1] + 16 + np.abs(logits[t][np.isfinite(logits[t])]).max(initial=0.0)) * 2.0 ** -23
+            bound[t] += p * ((b @ np.abs(down[e]).T) + (terms(n_h) + topk * 2.0 ** -23 + ep) * mag)[0]
+    return y, bound

@@ -52,6 +52,38 @@ def test_null_handles(lib):
     assert lib.glq_fp8_info(None, None, None, None) == 1
 
 
+@pytest.mark.parametrize("change,status", [
+    ({"experts": 0}, 2), ({"experts": 513}, 2), ({"d": 12}, 2), ({"inter": 0}, 2), ({"topk": 0}, 2), ({"topk": 9}, 2),
+    ({"experts": 20, "topk": 17}, 2), ({"experts": 16, "d": 1 << 20, "inter": 1 << 20}, 2), ({"scoring": 2}, 1), ({"routed_scale": float("inf")}, 1),
+])
+def test_moe_create_refusals(lib, change, status):
+    import e8_lattice_codebook_b200 as glq
+    base = dict(experts=8, d=128, inter=128, topk=2, scoring=0, renormalize=1, routed_scale=1.0)
+    h = ctypes.c_void_p(5)
+    assert lib.glq_moe_create(glq.MoeConfig(**{**base, **change}), P, P, P, P, P, P, None, ctypes.byref(h)) == status
+    assert not h.value
+    config = glq.MoeConfig(**base)
+    for i in range(6):
+        w = [P] * 6
+        w[i] = None
+        assert lib.glq_moe_create(config, *w, None, ctypes.byref(h)) == 1
+    assert lib.glq_moe_create(None, P, P, P, P, P, P, None, ctypes.byref(h)) == 1
+    assert lib.glq_moe_forward(None, P, 0, P, 0, P, 0, 1, None) == 1
+    assert lib.glq_moe_reserve(None, 1) == 1
+    assert lib.glq_moe_check(None, None) == 1
+    assert lib.glq_moe_destroy(None) == 1
+    assert lib.glq_moe_info(None, None, None) == 1
+
+
+def test_reference_routes_ties_to_the_lowest_index():
+    rows = np.array([[0.0, 1.0, 1.0, 1.0], [-np.inf, -np.inf, 2.0, -np.inf], [np.nan, 0.0, np.nan, 0.0], [-np.inf] * 4])
+    got = ref.route(rows, 2, True, 0, 1.0)
+    assert [[e for e, _ in r] for r in got] == [[1, 2], [2], [1, 3], []]
+    assert got[0][0][1] == 0.5 and got[1][0][1] == 1.0
+    every = ref.route(rows[:1], 1, False, 0, 2.0)[0][0][1]
+    assert abs(every - 2 * np.e / (1 + 3 * np.e)) < 1e-15
+
+
 def test_reference_rounds_as_the_format_does():
     """Every e4m3 value, the points half way between two, and their neighbours."""
     v = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
