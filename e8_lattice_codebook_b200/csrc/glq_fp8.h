@@ -78,6 +78,23 @@ Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, const int clusters[9]);
 cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, const CUtensorMap &qmap, int source, int nt, int clusters,
                               cudaStream_t s, bool pdl);
 
+// y [B][m] = x W^T for many tokens, tiles of FP8_GEMM_TOK tokens x 256 rows
+constexpr int FP8_GEMM_TOK = 256;
+struct Fp8GemmParams {
+    const float *ws;
+    const float *s;     // [KB][s_ld]
+    int64_t s_ld;
+    void *y;
+    int y_dtype;
+    int m, B, RT, KB;
+    int TT, tiles;      // token tiles; all tiles, token tiles within a column of them
+    unsigned *err;
+};
+// qmap: boxes of 128 columns x 128 tokens of q, 128-byte swizzle; wmap: the
+// laid-out weights as rows of 128 bytes, boxes of 128 rows, no swizzle
+cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const CUtensorMap &qmap, const CUtensorMap &wmap, int num_sms,
+                            cudaStream_t s, bool pdl);
+
 // A mixture-of-experts layer (glq_moe.cu) for T <= MOE_MAX_T tokens.  d: width
 // of x and y, inter: of an expert; KB1 = ceil(d/128) = DB, IB = ceil(inter/128).
 constexpr int MOE_MAX_T = 64, MOE_MAX_E = 512, MOE_MAX_K = 16;

@@ -41,8 +41,9 @@ glq_status launched(cudaError_t e) {
 }
 
 // TMA descriptor of e4m3 rows [rows][cols]: boxes of 128 columns x box_rows,
-// 128-byte swizzle, zero fill past the last row.
-bool encode_rows(CUtensorMap *map, const uint8_t *q, int64_t cols, int64_t rows, int box_rows) {
+// zero fill past the last row; 128-byte swizzle, or none for weights that are
+// laid out swizzled.
+bool encode_rows(CUtensorMap *map, const uint8_t *q, int64_t cols, int64_t rows, int box_rows, bool swizzle = true) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         cudaDriverEntryPointQueryResult r;
         void *fn = nullptr;
@@ -59,7 +60,8 @@ bool encode_rows(CUtensorMap *map, const uint8_t *q, int64_t cols, int64_t rows,
     const cuuint32_t box[2] = {GLQ_FP8_BLOCK, (cuuint32_t)box_rows};
     const cuuint32_t step[2] = {1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(q), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -73,6 +75,9 @@ void free_fp8(glq_fp8 L) {
 // Batches whose activations the product itself rounds; above, a kernel of
 // their own rounds them first.
 bool rounds_inside(int64_t B) { return B <= glq::FP8_ROUND_MAX; }
+
+// Batches for the many-token kernel.
+bool many_tokens(int64_t B) { return B > 64; }
 
 // What a call of B tokens needs of the shared workspace.
 void fp8_need(glq_fp8 L, int64_t B, bool quantized, size_t need[glq::FP8_WS_COUNT]) {
@@ -106,6 +111,26 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
         q = p.q;
         s = p.s;
         s_ld = B;
+    }
+    if (many_tokens(B)) {
+        glq::Fp8GemmParams p{};
+        p.ws = L->d_ws;
+        p.s = s;
+        p.s_ld = s_ld;
+        p.y = y;
+        p.y_dtype = y_dtype;
+        p.m = (int)L->m;
+        p.B = (int)B;
+        p.RT = L->RT;
+        p.KB = L->KB;
+        p.TT = (int)((B + glq::FP8_GEMM_TOK - 1) / glq::FP8_GEMM_TOK);
+        p.tiles = (L->RT + 1) / 2 * p.TT;
+        p.err = L->d_err;
+        CUtensorMap qmap, wmap;
+        if (!encode_rows(&qmap, q, (int64_t)L->KB * GLQ_FP8_BLOCK, B, 128) ||
+            !encode_rows(&wmap, L->d_w, GLQ_FP8_BLOCK, (int64_t)L->RT * L->KB * 128, 128, false))
+            return GLQ_ERR_CUDA;
+        return launched(glq::launch_fp8_gemm(p, qmap, wmap, L->num_sms, st, true));
     }
     glq::Fp8SkinnyParams p{};
     p.w = L->d_w;
