@@ -12,7 +12,7 @@
 //   * tokens are the M side: a thread of the drain owns one token and 128
 //     columns of one 128-row weight block, so that a K block has one scale per
 //     thread, and the sums stay in its registers (128 of them) until the tile
-//     ends: 64 packed fused multiply-adds per thread and K block;
+//     ends: 128 fused multiply-adds per thread and K block;
 //   * two accumulators of 256 TMEM columns: the MMAs of one K block run while
 //     the other one is drained.
 // Warps: 0 copies (TMA of the e4m3 rows and of the laid-out weight tiles, both
@@ -52,12 +52,6 @@ __device__ __forceinline__ void mma2_f8_ss(uint32_t d_tmem, uint64_t a_desc, uin
         : "memory");
 }
 
-// acc (a pair of fp32) += d * f
-__device__ __forceinline__ void fma_pair(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t f) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(f));
-}
 // arrive on the barrier at the same place in the pair's first CTA
 __device__ __forceinline__ void arrive_first(uint64_t *bar) {
     asm volatile(
@@ -65,17 +59,6 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar) {
         " mbarrier.arrive.shared::cluster.b64 _, [ra];\n}\n" ::"r"(smem_addr(bar))
         : "memory");
 }
-__device__ __forceinline__ uint64_t pair(float v) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(__float_as_uint(v)));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-    uint32_t a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-    return make_float2(__uint_as_float(a), __uint_as_float(b));
-}
-
 __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_constant__ CUtensorMap qmap,
                                                               const __grid_constant__ CUtensorMap wmap,
                                                               Fp8GemmParams p) {
@@ -199,9 +182,9 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
             const int rt = 2 * ct + half;
             const float *s = p.s + min(token, p.B - 1);
             const float *ws = p.ws + (int64_t)min(rt, p.RT - 1) * KB;
-            uint64_t acc[64];
+            float acc[128];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0;
+            for (int j = 0; j < 128; ++j) acc[j] = 0.f;
             // scales four blocks ahead: a load takes longer than a block's MMAs
             float next[4], now[4];
             auto fetch = [&](int kb) {
@@ -222,20 +205,23 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok) break;
                     sm100::tc_fence_after();
-                    const uint64_t f = pair(now[i]);
+                    const float f = now[i];
                     uint32_t d[2][32];
                     sm100::tmem_ld32(t0 + a * COLS, d[0]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         sm100::tmem_wait_ld();
-                        if (c < 3) sm100::tmem_ld32(t0 + a * COLS + (c + 1) * 32, d[(c + 1) & 1]);
+                        if (c < 3) {
+                            sm100::tmem_ld32(t0 + a * COLS + (c + 1) * 32, d[(c + 1) & 1]);
+                        } else {  // all read: the MMAs of the block after next may start
+                            sm100::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_first(&acc_empty[a]);
+                        }
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            fma_pair(acc[c * 16 + j], d[c & 1][2 * j], d[c & 1][2 * j + 1], f);
+                        for (int j = 0; j < 32; ++j)
+                            acc[c * 32 + j] = fmaf(__uint_as_float(d[c & 1][j]), f, acc[c * 32 + j]);
                     }
-                    sm100::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_first(&acc_empty[a]);
                     a ^= 1;
                     if (a == 0) apar ^= 1;
                 }
@@ -244,11 +230,10 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
             if (token < p.B && rt < p.RT) {
                 const int row0 = rt * 128;
 #pragma unroll
-                for (int j = 0; j < 64; j += 2) {
-                    const float2 u = unpair(acc[j]), v = unpair(acc[j + 1]);
-                    if (row0 + 2 * j < p.m)  // m is a multiple of 8: four columns are in or out together
-                        store_y4(p.y, p.y_dtype, (int64_t)token * p.m + row0 + 2 * j, make_float4(u.x, u.y, v.x, v.y));
-                }
+                for (int j = 0; j < 128; j += 4)
+                    if (row0 + j < p.m)  // m is a multiple of 8: four columns are in or out together
+                        store_y4(p.y, p.y_dtype, (int64_t)token * p.m + row0 + j,
+                                 make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
             }
         }
     }
