@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
             // parts to the CTAs that sum them
             const int mine = live > (int)rank ? (live - (int)rank - 1) / (int)C + 1 : 0;  // tokens this CTA sums
             if (!met) cluster_wait(), met = true;
-            if (!pipe.wait_warp_cluster(&pipe.red_empty, (round & 1) ^ 1, p.err)) break;
+            if (!pipe.wait_warp(&pipe.red_empty, (round & 1) ^ 1, p.err)) break;
             if (dtid == 0) mbar_expect_tx(&pipe.red_full, (uint32_t)(mine * (int)C) * 512);
 #pragma unroll
             for (int j = 0; j < HALF; ++j) {
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
                     st_async(remote_smem(red + ((int)rank * per + own) * 128 + row_l, to), acc[j],
                              remote_smem(&pipe.red_full, to));
             }
-            if (!pipe.wait_warp_cluster(&pipe.red_full, round & 1, p.err)) break;
+            if (!pipe.wait_warp(&pipe.red_full, round & 1, p.err)) break;
             // a warp sums one token in eight, a lane four rows
             const int row = rt * 128 + lane * 4;
             for (int own = dtid >> 5; own < mine; own += D_WARPS) {

@@ -93,6 +93,45 @@ __device__ __forceinline__ uint32_t round4(uint2 w, float inv) {
 }
 
 // ---------------------------------------------------------------------------
+// Waits poll with test_wait, which answers at once.  A try_wait that suspends
+// its thread holds up the waits of the other warps on its scheduler (the
+// drain warps beside the MMA thread saw their barrier 0.5 us after the rest).
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// false once the wait has run out, here (then *abort is set and the error
+// word says so) or elsewhere in the CTA
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned *err) {
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t t0 = sm100::clock_cycles();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i) {
+            if (mbar_test(bar, parity)) return true;
+#ifdef NAP
+            __nanosleep(NAP);
+#endif
+        }
+        if (*abort) return false;
+        if (sm100::clock_cycles() - t0 > WAIT_CYCLES) {
+            atomicOr(err, GLQ_DEVERR_TIMEOUT);
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // tcgen05.mma kind::f8f6f4, e4m3 x e4m3 -> fp32, K = 32 per instruction
 // ---------------------------------------------------------------------------
 
@@ -220,20 +259,8 @@ struct Pipe {
         atomicOr(err, GLQ_DEVERR_TIMEOUT);
         abort = 1;
     }
-    // false once the wait has run out, here or elsewhere in the CTA
     __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, unsigned *err) {
-        if (sm100::mbar_try(bar, parity)) return true;
-        const uint64_t t0 = sm100::clock_cycles();
-        for (;;) {
-#pragma unroll 1
-            for (int i = 0; i < 64; ++i)
-                if (sm100::mbar_try(bar, parity)) return true;
-            if (abort) return false;
-            if (sm100::clock_cycles() - t0 > WAIT_CYCLES) {
-                fail(err);
-                return false;
-            }
-        }
+        return wait_bounded(bar, parity, &abort, err);
     }
     // The same for a whole warp: one lane waits and __syncwarp orders the
     // others after it.  A poll by all 32 lanes takes the mbarrier unit 32
@@ -241,16 +268,6 @@ struct Pipe {
     __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, unsigned *err) {
         bool ok = true;
         if ((threadIdx.x & 31) == 0) ok = wait(bar, parity, err);
-        __syncwarp();
-        return __shfl_sync(0xffffffffu, ok, 0);
-    }
-    // on a barrier that other CTAs of the cluster arrive on
-    __device__ __forceinline__ bool wait_warp_cluster(uint64_t *bar, uint32_t parity, unsigned *err) {
-        bool ok = true;
-        if ((threadIdx.x & 31) == 0) {
-            ok = sm100::mbar_wait_cluster(bar, parity, WAIT_CYCLES);
-            if (!ok) fail(err);
-        }
         __syncwarp();
         return __shfl_sync(0xffffffffu, ok, 0);
     }

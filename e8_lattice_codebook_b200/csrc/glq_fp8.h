@@ -91,9 +91,10 @@ struct Fp8GemmParams {
     unsigned *err;
 };
 // qmap: boxes of 128 columns x 128 tokens of q, 128-byte swizzle; wmap: the
-// laid-out weights as rows of 128 bytes, boxes of 128 rows, no swizzle
-cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const CUtensorMap &qmap, const CUtensorMap &wmap, int num_sms,
-                            cudaStream_t s, bool pdl);
+// laid-out weights as rows of 128 bytes, boxes of 64 rows, no swizzle; ymap:
+// boxes of 128 bytes x 32 tokens of y, 128-byte swizzle
+cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const CUtensorMap &qmap, const CUtensorMap &wmap,
+                            const CUtensorMap &ymap, int num_sms, cudaStream_t s, bool pdl);
 
 // A mixture-of-experts layer (glq_moe.cu) for T <= MOE_MAX_T tokens.  d: width
 // of x and y, inter: of an expert; KB1 = ceil(d/128) = DB, IB = ceil(inter/128).

@@ -40,10 +40,11 @@ glq_status launched(cudaError_t e) {
     return GLQ_ERR_CUDA;
 }
 
-// TMA descriptor of e4m3 rows [rows][cols]: boxes of 128 columns x box_rows,
-// zero fill past the last row; 128-byte swizzle, or none for weights that are
-// laid out swizzled.
-bool encode_rows(CUtensorMap *map, const uint8_t *q, int64_t cols, int64_t rows, int box_rows, bool swizzle = true) {
+// TMA descriptor of rows [rows][cols] of `type` (`size` bytes each): boxes of
+// 128 bytes x box_rows, zero fill past the last row; 128-byte swizzle, or none
+// for weights that are laid out swizzled.
+bool encode_rows(CUtensorMap *map, CUtensorMapDataType type, int size, const void *base, int64_t cols, int64_t rows,
+                 int box_rows, bool swizzle = true) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         cudaDriverEntryPointQueryResult r;
         void *fn = nullptr;
@@ -56,13 +57,15 @@ bool encode_rows(CUtensorMap *map, const uint8_t *q, int64_t cols, int64_t rows,
     }();
     if (!encode) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)cols};
-    const cuuint32_t box[2] = {GLQ_FP8_BLOCK, (cuuint32_t)box_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(cols * size)};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows};
     const cuuint32_t step[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(q), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return encode(map, type, 2, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_e4m3(CUtensorMap *map, const uint8_t *q, int64_t cols, int64_t rows, int box_rows, bool swizzle = true) {
+    return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q, cols, rows, box_rows, swizzle);
 }
 
 void free_fp8(glq_fp8 L) {
@@ -126,11 +129,13 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
         p.TT = (int)((B + glq::FP8_GEMM_TOK - 1) / glq::FP8_GEMM_TOK);
         p.tiles = (L->RT + 1) / 2 * p.TT;
         p.err = L->d_err;
-        CUtensorMap qmap, wmap;
-        if (!encode_rows(&qmap, q, (int64_t)L->KB * GLQ_FP8_BLOCK, B, 128) ||
-            !encode_rows(&wmap, L->d_w, GLQ_FP8_BLOCK, (int64_t)L->RT * L->KB * 128, 128, false))
+        CUtensorMap qmap, wmap, ymap;
+        if (!encode_e4m3(&qmap, q, (int64_t)L->KB * GLQ_FP8_BLOCK, B, 128) ||
+            !encode_e4m3(&wmap, L->d_w, GLQ_FP8_BLOCK, (int64_t)L->RT * L->KB * 128, 64, false) ||
+            !encode_rows(&ymap, y_dtype == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                         y_dtype == 2 ? 4 : 2, y, L->m, B, 32))
             return GLQ_ERR_CUDA;
-        return launched(glq::launch_fp8_gemm(p, qmap, wmap, L->num_sms, st, true));
+        return launched(glq::launch_fp8_gemm(p, qmap, wmap, ymap, L->num_sms, st, true));
     }
     glq::Fp8SkinnyParams p{};
     p.w = L->d_w;
@@ -150,7 +155,7 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
     const glq::Fp8SkinnyPlan plan = glq::plan_fp8_skinny((int64_t)p.RT * p.TT, p.KB, L->clusters);
     p.C = plan.C;
     CUtensorMap qmap{};
-    if (source == 2 && !encode_rows(&qmap, q, (int64_t)L->KB * GLQ_FP8_BLOCK, B, nt)) return GLQ_ERR_CUDA;
+    if (source == 2 && !encode_e4m3(&qmap, q, (int64_t)L->KB * GLQ_FP8_BLOCK, B, nt)) return GLQ_ERR_CUDA;
     return launched(glq::launch_fp8_skinny(p, qmap, source, nt, plan.clusters, st, true));
 }
 

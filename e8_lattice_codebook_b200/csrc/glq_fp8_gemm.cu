@@ -6,15 +6,18 @@
 // K block at a time; its result is scaled and added in registers.  What bounds
 // the kernel is the MMA, if that second sum keeps up:
 //   * tiles of 256 tokens x 256 weight rows per cluster of two CTAs
-//     (cta_group::2, M = 256, N = 256: 128 tokens per CTA, each CTA holding
+//     (cta_group::2, M = 256: 128 tokens per CTA, each CTA holding
 //     half of the weight rows' operand), so that a CTA copies 32 KB for the
 //     512 cycles of a K block's MMAs;
 //   * tokens are the M side: a thread of the drain owns one token and 128
 //     columns of one 128-row weight block, so that a K block has one scale per
 //     thread, and the sums stay in its registers (128 of them) until the tile
 //     ends: 128 fused multiply-adds per thread and K block;
-//   * two accumulators of 256 TMEM columns: the MMAs of one K block run while
-//     the other one is drained.
+//   * the two 128-row blocks of a tile are MMAs of their own (N = 128), each
+//     with two accumulators of 128 TMEM columns and its own four drain warps:
+//     from an accumulator's MMAs to its reuse pass the MMA's latency, the read
+//     and an arrival from the other CTA, and the more pieces wait for that
+//     apart, the more of them the MMAs cover.
 // Warps: 0 copies (TMA of the e4m3 rows and of the laid-out weight tiles, both
 // completing on the first CTA's barrier), 1 MMA (first CTA) and TMEM, 4-11
 // drain.  Every wait is bounded; a timeout sets the layer's error word.
@@ -28,17 +31,41 @@ namespace {
 using namespace fp8;
 
 constexpr int TOK = 128;                  // tokens per CTA
-constexpr int COLS = 256;                 // weight rows of a tile
-constexpr int A_BYTES = TOK * 128, B_BYTES = GLQ_FP8_TILE_BYTES;
-constexpr int STAGE = A_BYTES + B_BYTES;  // 32 KB
-constexpr int STAGES = 6;
+constexpr int COLS = 128;                 // weight rows of one of a tile's two MMAs
+constexpr int A_BYTES = TOK * 128, B_BYTES = GLQ_FP8_TILE_BYTES / 2;  // half of each block's rows per CTA
+constexpr int STAGE = A_BYTES + 2 * B_BYTES;  // 32 KB
+constexpr int STAGES = 5;
 constexpr int DRAIN_WARPS = 8;
 // warps 0-3: copies, MMA, two idle; 4-11: drain.  Registers move between the
 // warpgroups: 384 threads start with 168 each; the first warpgroup keeps 56,
 // the two that drain hold 224 (128 x 56 + 256 x 224 = 384 x 168).
 constexpr int DRAIN_WARP0 = 4;
 constexpr int THREADS = (DRAIN_WARP0 + DRAIN_WARPS) * 32;
-constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE;
+// y leaves by TMA from shared memory, a drain warp's 32 tokens in chunks of 128
+// bytes of columns, two at a time (stores from the threads, which own a token
+// each, would touch 32 rows per instruction: a quarter of the kernel's time at
+// 32 K blocks).
+constexpr int CHUNK = 32 * 128;
+constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + (size_t)DRAIN_WARPS * 2 * CHUNK;
+
+// Chunk (c0, c1) of y from shared memory; rows and columns past y are left out.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(smem_addr(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
+    if (dtype == 1) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
 
 __device__ __forceinline__ void mma2_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -61,12 +88,13 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar) {
 }
 __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_constant__ CUtensorMap qmap,
                                                               const __grid_constant__ CUtensorMap wmap,
+                                                              const __grid_constant__ CUtensorMap ymap,
                                                               Fp8GemmParams p) {
     extern __shared__ uint8_t smem_raw[];
     // (first CTA) full: both CTAs' copies have landed; acc_empty: both CTAs have
     // drained the accumulator.  (both) empty: the MMAs of the stage have
     // finished; acc_full: the accumulator holds a K block.
-    __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], mma_done;
+    __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[4], acc_empty[4], mma_done;  // accumulator 2 half + turn
     __shared__ uint32_t tmem_holder;
     __shared__ volatile int abort_flag;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -79,14 +107,15 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < 4; ++a) {
             mbar_init(&acc_full[a], 1);
-            mbar_init(&acc_empty[a], 2 * DRAIN_WARPS);
+            mbar_init(&acc_empty[a], DRAIN_WARPS);  // four of each CTA
         }
         mbar_init(&mma_done, 1);
         abort_flag = 0;
         sm100::prefetch_tensormap(&qmap);
         sm100::prefetch_tensormap(&wmap);
+        sm100::prefetch_tensormap(&ymap);
     }
     if (warp == 1) {
         sm100::tmem_alloc2(&tmem_holder, 512);
@@ -99,20 +128,10 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
     const uint32_t tmem = tmem_holder;
     pdl_launch_dependents();
 
-    auto fail = [&]() {
-        atomicOr(p.err, GLQ_DEVERR_TIMEOUT);
-        abort_flag = 1;
-    };
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        // CTA scope: what the barriers order is copies, MMAs and TMEM loads (the
-        // tcgen05 fences), no stores of another CTA.  Cluster-scope acquires, one
-        // per drain warp and K block, cost more than the K block's MMAs.
-        if (sm100::mbar_try(bar, parity)) return true;
-        if (abort_flag) return false;
-        if (sm100::mbar_wait(bar, parity, WAIT_CYCLES)) return true;
-        fail();
-        return false;
-    };
+    // CTA scope: what the barriers order is copies, MMAs and TMEM loads (the
+    // tcgen05 fences), no stores of another CTA.  Cluster-scope acquires, one
+    // per drain warp and K block, cost more than the K block's MMAs.
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bounded(bar, parity, &abort_flag, p.err); };
     const int KB = p.KB;
 
     if (warp < DRAIN_WARP0) {
@@ -124,16 +143,17 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
             bool ok = true;
             for (int tile = cid; tile < p.tiles && ok; tile += ncl) {
                 const int ct = tile / p.TT, tt = tile - ct * p.TT;
-                const int tok0 = tt * (2 * TOK) + (int)rank * TOK, rt = 2 * ct + (int)rank;
-                const bool mine = rt < p.RT;                     // this CTA's weight rows exist
-                const uint32_t bytes = 2 * A_BYTES + (2 * ct + 1 < p.RT ? 2 : 1) * B_BYTES;
-                int wrow = rt * KB * 128;
+                const int tok0 = tt * (2 * TOK) + (int)rank * TOK;
+                const bool both = 2 * ct + 1 < p.RT;             // the second block of weight rows exists
+                const uint32_t bytes = 2 * (A_BYTES + (both ? 2 : 1) * B_BYTES);
+                int wrow = 2 * ct * KB * 128 + (int)rank * 64;   // this CTA's 64 rows of a block
                 for (int kb = 0; kb < KB; ++kb, wrow += 128) {
                     if (!(ok = wait(&empty[s], par))) break;
                     uint8_t *st = smem + s * STAGE;
                     if (rank == 0) mbar_expect_tx(&full[s], bytes);
                     sm100::tma_load_2d_pair(st, &qmap, &full[s], kb * GLQ_FP8_BLOCK, tok0);
-                    if (mine) sm100::tma_load_2d_pair(st + A_BYTES, &wmap, &full[s], 0, wrow);
+                    sm100::tma_load_2d_pair(st + A_BYTES, &wmap, &full[s], 0, wrow);
+                    if (both) sm100::tma_load_2d_pair(st + A_BYTES + B_BYTES, &wmap, &full[s], 0, wrow + KB * 128);
                     ++loaded;
                     if (++s == STAGES) s = 0, par ^= 1;
                 }
@@ -150,13 +170,20 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
                 bool ok = true;
                 for (int tile = cid; tile < p.tiles && ok; tile += ncl) {
                     for (int kb = 0; kb < KB; ++kb) {
-                        if (!(ok = wait(&acc_empty[a], apar) && wait(&full[s], par))) break;
-                        sm100::tc_fence_after();
+                        if (!(ok = wait(&full[s], par))) break;
                         uint8_t *st = smem + s * STAGE;
-                        const uint64_t ad = sm100::smem_desc_sw128(st), bd = sm100::smem_desc_sw128(st + A_BYTES);
+                        const uint64_t ad = sm100::smem_desc_sw128(st);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) mma2_f8_ss(tmem + a * COLS, ad + 2 * kk, bd + 2 * kk, idesc, kk);
-                        sm100::mma2_commit_both(&acc_full[a]);
+                        for (int h = 0; h < 2; ++h) {
+                            if (!(ok = wait(&acc_empty[2 * h + a], apar))) break;
+                            sm100::tc_fence_after();
+                            const uint64_t bd = sm100::smem_desc_sw128(st + A_BYTES + h * B_BYTES);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma2_f8_ss(tmem + (2 * h + a) * COLS, ad + 2 * kk, bd + 2 * kk, idesc, kk);
+                            sm100::mma2_commit_both(&acc_full[2 * h + a]);
+                        }
+                        if (!ok) break;
                         sm100::mma2_commit_both(&empty[s]);
                         if (++s == STAGES) s = 0, par ^= 1;
                         a ^= 1;
@@ -173,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
         // ---------------- drain ----------------
         pdl_wait();  // scales of the tokens; y may still be in use by the kernel before
         const int quadrant = warp & 3, half = (warp - DRAIN_WARP0) >> 2;
-        const uint32_t t0 = tmem + ((uint32_t)(32 * quadrant) << 16) + half * 128;
+        const uint32_t t0 = tmem + ((uint32_t)(32 * quadrant) << 16) + half * 2 * COLS;
         uint32_t a = 0, apar = 0;
         bool ok = true;
         for (int tile = cid; tile < p.tiles && ok; tile += ncl) {
@@ -185,27 +212,31 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
             float acc[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) acc[j] = 0.f;
-            // scales four blocks ahead: a load takes longer than a block's MMAs
-            float next[4], now[4];
-            auto fetch = [&](int kb) {
+            // Four blocks' scales are loaded while the four before them are used,
+            // and multiplied after: a product of values still on their way would
+            // stop the warp.
+            float f[4], rs[4], rw[4];
+            auto fetch = [&](int kb0) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    next[i] = kb + i < KB ? __ldg(s + (int64_t)(kb + i) * p.s_ld) * __ldg(ws + kb + i) : 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    const int kb = min(kb0 + i, KB - 1);
+                    rs[i] = __ldg(s + (int64_t)kb * p.s_ld);
+                    rw[i] = __ldg(ws + kb);
+                }
             };
             fetch(0);
             for (int kb0 = 0; kb0 < KB && ok; kb0 += 4) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) now[i] = next[i];
+                for (int i = 0; i < 4; ++i) f[i] = rs[i] * rw[i];
                 fetch(kb0 + 4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (kb0 + i >= KB) break;
-                    if (lane == 0) ok = wait(&acc_full[a], apar);
+                    if (lane == 0) ok = wait(&acc_full[2 * half + a], apar);
                     __syncwarp();
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok) break;
                     sm100::tc_fence_after();
-                    const float f = now[i];
                     uint32_t d[2][32];
                     sm100::tmem_ld32(t0 + a * COLS, d[0]);
 #pragma unroll
@@ -216,26 +247,63 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
                         } else {  // all read: the MMAs of the block after next may start
                             sm100::tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) arrive_first(&acc_empty[a]);
+                            if (lane == 0) arrive_first(&acc_empty[2 * half + a]);
                         }
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            acc[c * 32 + j] = fmaf(__uint_as_float(d[c & 1][j]), f, acc[c * 32 + j]);
+                            acc[c * 32 + j] = fmaf(__uint_as_float(d[c & 1][j]), f[i], acc[c * 32 + j]);
                     }
                     a ^= 1;
                     if (a == 0) apar ^= 1;
                 }
             }
             if (!ok) break;
-            if (token < p.B && rt < p.RT) {
-                const int row0 = rt * 128;
+            const int row0 = rt * 128, tok0 = token - lane;
+            uint8_t *out = smem + STAGES * STAGE + (warp - DRAIN_WARP0) * 2 * CHUNK + lane * 128;
+            // 64 columns of a 16-bit y, or 32 of fp32, to a chunk
+            auto put = [&](auto chunk_words, int c, int slot) {
+                uint8_t *row = out + slot * CHUNK;
 #pragma unroll
-                for (int j = 0; j < 128; j += 4)
-                    if (row0 + j < p.m)  // m is a multiple of 8: four columns are in or out together
-                        store_y4(p.y, p.y_dtype, (int64_t)token * p.m + row0 + j,
-                                 make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4 *>(row + ((j ^ (lane & 7)) << 4)) = chunk_words(c, j);
+            };
+            auto send = [&](int col, int slot) {
+                if (col < p.m && tok0 < p.B)
+                    sm100::fence_proxy_async_smem(), __syncwarp();
+                if (lane == 0 && col < p.m && tok0 < p.B) {
+                    tma_store_2d(&ymap, out - lane * 128 + slot * CHUNK, col, tok0);
+                    bulk_commit();
+                }
+            };
+            if (lane == 0) bulk_wait_read();  // the last tile's chunks have been read
+            __syncwarp();
+            if (p.y_dtype == 2) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c == 2) {
+                        if (lane == 0) bulk_wait_read();
+                        __syncwarp();
+                    }
+                    put([&](int k, int j) {
+                        const float *v = acc + k * 32 + j * 4;
+                        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                          __float_as_uint(v[3]));
+                    }, c, c & 1);
+                    send(row0 + c * 32, c & 1);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    put([&](int k, int j) {
+                        const float *v = acc + k * 64 + j * 8;
+                        return make_uint4(pack2(v[0], v[1], p.y_dtype), pack2(v[2], v[3], p.y_dtype),
+                                          pack2(v[4], v[5], p.y_dtype), pack2(v[6], v[7], p.y_dtype));
+                    }, c, c);
+                    send(row0 + c * 64, c);
+                }
             }
         }
+        if (lane == 0) bulk_wait_all();  // before the CTA's shared memory is given back
     }
     __syncwarp();
     sm100::tc_fence_before();
@@ -249,8 +317,8 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
 
 }  // namespace
 
-cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const CUtensorMap &qmap, const CUtensorMap &wmap, int num_sms,
-                            cudaStream_t s, bool pdl) {
+cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const CUtensorMap &qmap, const CUtensorMap &wmap,
+                            const CUtensorMap &ymap, int num_sms, cudaStream_t s, bool pdl) {
     const void *fn = (const void *)fp8_gemm_kernel;
     static std::atomic<uint64_t> configured;
     const cudaError_t e = once_per_device(configured, [fn] {
@@ -258,8 +326,8 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const CUtensorMap &qmap, con
     });
     if (e != cudaSuccess) return e;
     Fp8GemmParams q = p;
-    CUtensorMap a = qmap, b = wmap;
-    void *args[] = {&a, &b, &q};
+    CUtensorMap a = qmap, b = wmap, c = ymap;
+    void *args[] = {&a, &b, &c, &q};
     const int clusters = p.tiles < num_sms / 2 ? p.tiles : num_sms / 2;
     return launch_ex(fn, dim3(2 * clusters), dim3(THREADS), SMEM, s, pdl, args, 2);
 }
