@@ -237,21 +237,22 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok) break;
                     sm100::tc_fence_after();
-                    uint32_t d[2][32];
-                    sm100::tmem_ld32(t0 + a * COLS, d[0]);
+                    // a read takes about 190 cycles beside the MMAs, whatever its
+                    // size: 64 columns at a time
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 128; c += 64) {
+                        uint32_t d[2][32];
+                        sm100::tmem_ld32(t0 + a * COLS + c, d[0]);
+                        sm100::tmem_ld32(t0 + a * COLS + c + 32, d[1]);
                         sm100::tmem_wait_ld();
-                        if (c < 3) {
-                            sm100::tmem_ld32(t0 + a * COLS + (c + 1) * 32, d[(c + 1) & 1]);
-                        } else {  // all read: the MMAs of the block after next may start
+                        if (c == 64) {  // all read: the MMAs of the block after next may start
                             sm100::tc_fence_before();
                             __syncwarp();
                             if (lane == 0) arrive_first(&acc_empty[2 * half + a]);
                         }
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            acc[c * 32 + j] = fmaf(__uint_as_float(d[c & 1][j]), f[i], acc[c * 32 + j]);
+                        for (int j = 0; j < 64; ++j)
+                            acc[c + j] = fmaf(__uint_as_float(d[j >> 5][j & 31]), f[i], acc[c + j]);
                     }
                     a ^= 1;
                     if (a == 0) apar ^= 1;
