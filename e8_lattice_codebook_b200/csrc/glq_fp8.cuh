@@ -358,7 +358,7 @@ template <int NT, int N, bool SKIP_ZERO>
 __device__ __forceinline__ bool pipe_drain(Pipe<NT> &p, uint32_t it, int quadrant, int set, float (&acc)[NT / 2],
                                            unsigned *err) {
     constexpr int HALF = NT / 2, STAGES = Pipe<NT>::STAGES;
-    constexpr int STEP = HALF < 16 ? 8 : 16;
+    constexpr int STEP = HALF < 32 ? HALF : 32;
     const uint32_t last = it + N - 1;
     if (!p.wait_warp(&p.done[last % STAGES], (last / STAGES) & 1, err)) return false;
     sm100::tc_fence_after();
@@ -372,7 +372,8 @@ __device__ __forceinline__ bool pipe_drain(Pipe<NT> &p, uint32_t it, int quadran
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             if constexpr (STEP == 8) tmem_ld8(t0 + s[n] * NT + c, d[n]);
-            else sm100::tmem_ld16(t0 + s[n] * NT + c, d[n]);
+            else if constexpr (STEP == 16) sm100::tmem_ld16(t0 + s[n] * NT + c, d[n]);
+            else sm100::tmem_ld32(t0 + s[n] * NT + c, d[n]);
         }
         sm100::tmem_wait_ld();
 #pragma unroll
