@@ -445,6 +445,8 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
             }
         }
     }
+    // converged, or a warp whose one thread is still at work counts twice
+    __syncwarp();
     sm100::tc_fence_before();
     __syncthreads();
     if (copier && pipe.abort) pipe_load_drain(pipe, it);
