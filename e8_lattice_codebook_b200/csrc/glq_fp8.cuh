@@ -423,6 +423,7 @@ __device__ __forceinline__ uint32_t range_begin(uint32_t c, uint32_t total, uint
 }
 // the CTA that owns block b
 __device__ __forceinline__ int range_owner(uint32_t b, uint32_t total, uint32_t G) {
+    if (total <= 0xFFFFFFFFu / G) return (int)(((b + 1) * G - 1) / total);  // a 64-bit division takes four times as long
     return (int)((((uint64_t)b + 1) * G - 1) / total);
 }
 

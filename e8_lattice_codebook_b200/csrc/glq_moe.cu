@@ -37,6 +37,7 @@ constexpr int THREADS = WARPS * 32;           // 608
 constexpr int GRID_WARP = WARPS - 1;
 constexpr int H_WARPS = X_WARPS + D_WARPS;    // warps that form h^
 constexpr uint8_t NONE = 0xFF;
+constexpr int LOCAL_T = 4;
 
 // Shared memory behind the stages.
 struct Layout {
@@ -94,7 +95,7 @@ __device__ __forceinline__ void route(const MoeParams &p, int t, int lane, int16
             if (key[i]) sum += expf(key_logit(key[i]) - top);
         sum = warp_sum(sum);
     }
-    float mine = 0.f;  // lane j: the weight of choice j
+    uint32_t mine = 0, expert = 0;  // lane j: choice j's key and index
     for (int j = 0; j < p.k; ++j) {
         best = 0;
         uint32_t at = 0;
@@ -102,25 +103,23 @@ __device__ __forceinline__ void route(const MoeParams &p, int t, int lane, int16
         for (int i = NV - 1; i >= 0; --i)  // downwards: the lowest index of equals stays
             if (key[i] >= best) best = key[i], at = i * 32 + lane;
         const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+        if (m == 0) break;  // nothing left to choose
         const uint32_t e = __reduce_min_sync(0xffffffffu, best == m ? at : 0xFFFFFFFFu);
-        if (m == 0) {  // nothing left to choose
-            if (lane == 0) ids[j] = -1;
-            continue;
-        }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if ((uint32_t)(i * 32 + lane) == e) key[i] = 0;
-        const float l = key_logit(m);
-        const float w = p.scoring == 0 ? expf(l - top) : 1.f / (1.f + expf(-l));
-        if (p.renormalize) sum += w;
-        if (lane == j) mine = w;
-        if (lane == 0) {
-            ids[j] = (int16_t)e;
-            atomicOr(mask + e, 1ull << t);
-        }
+        if (lane == j) mine = m, expert = e;
     }
-    if (p.renormalize || p.scoring == 0) mine = mine / sum;
-    if (lane < p.k) wts[lane] = mine * p.routed_scale;
+    const float l = key_logit(mine);
+    float w = 0.f;
+    if (mine) w = p.scoring == 0 ? expf(l - top) : 1.f / (1.f + expf(-l));
+    if (p.renormalize) sum = warp_sum(w);
+    if (p.renormalize || p.scoring == 0) w = w / sum;
+    if (lane < p.k) {
+        ids[lane] = mine ? (int16_t)expert : (int16_t)-1;
+        wts[lane] = w * p.routed_scale;
+        if (mine) atomicOr(mask + expert, 1ull << t);
+    }
 }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
@@ -140,7 +139,31 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(
 
 __device__ __forceinline__ float silu(float v) { return v / (1.f + expf(-v)); }
 
-template <int NT>
+// A scale warp, block i: the group w of T tokens rounded into the operand tile.
+template <int NT, typename T16>
+__device__ __forceinline__ bool put_rounded(Pipe<NT> &pipe, uint8_t *smem, uint32_t i, const uint2 (&w)[LOCAL_T], int T,
+                                            float ws, int lane, unsigned *err) {
+    float inv;
+    const float s = warp_group_scales<T16, LOCAL_T>(w, T, lane, inv);
+    if (!pipe_x_begin(pipe, i, err)) return false;
+    uint8_t *xt = pipe_x_tile<NT>(smem, i);
+    if (lane < NT) pipe.sc[i % Pipe<NT>::STAGES][lane] = lane < T ? s * ws : 0.f;
+#pragma unroll
+    for (int t = 0; t < LOCAL_T; ++t) {
+        if (t >= T) break;
+        *reinterpret_cast<uint32_t *>(xt + sw128(t, lane >> 2) + (lane & 3) * 4) =
+            round4<T16>(w[t], __shfl_sync(0xffffffffu, inv, t));
+    }
+    pipe_x_done<NT, true>(pipe, i, lane);
+    return true;
+}
+
+// LOCAL (at most LOCAL_T tokens): x^ and h^ are not shared through memory;
+// every CTA rounds the tokens' columns that its own blocks need into its
+// operand tiles.  The work is done several times over, but two of the four
+// barriers, 2 to 4 us each while the weights saturate the memory, and h's trip
+// through memory go.
+template <int NT, bool LOCAL>
 __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
     using P = Pipe<NT>;
     constexpr int HALF = NT / 2, STAGES = P::STAGES, DRAIN = P::DRAIN;
@@ -177,7 +200,9 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
     }
     for (int e = tid; e < E; e += THREADS) mask[e] = 0;
     for (int i = tid; i < (int)(at.end - at.slot) / 4; i += THREADS) reinterpret_cast<uint32_t *>(slot)[i] = 0xFFFFFFFFu;
+    if (tid == 0) prefetch_l2(p.bar);  // before the weights are in flight
     // this CTA's share of x^: a warp per token and group
+    if constexpr (!LOCAL)
     for (int i = warp * G + cta; i < T * p.KB1; i += WARPS * G) {
         const int t = i / p.KB1, kb = i - t * p.KB1, col = kb * GLQ_FP8_BLOCK + lane * 4;
         uint2 w = make_uint2(0, 0);  // d is a multiple of 8: a lane's four columns are in or out together
@@ -190,7 +215,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
         __stcg(reinterpret_cast<uint32_t *>(p.xq + (int64_t)kb * (NT * 128) + sw128(t, lane >> 2)) + (lane & 3), q);
         if (lane == 0) __stcg(p.xs + kb * NT + t, s);
     }
-    fence_proxy_async();  // x^ is read by bulk copies
+    if (!LOCAL) fence_proxy_async();  // x^ is read by bulk copies
     __syncthreads();
     for (int t = warp; t < T; t += WARPS) {
         if (E <= 128) route<4>(p, t, lane, ids + t * K, wts + t * K, mask);
@@ -237,41 +262,57 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
         if (elect_one()) {
             copier = true;
             Loader<NT> ld(smem);
-            // one phase: the blocks [b, b + n), whose weight tiles are w(b) and
-            // token tiles x(b); the token tiles exist once `bar` completes
-            auto phase = [&](uint32_t b, uint32_t n, uint64_t *bar, auto w, auto x) {
-                const uint32_t ahead = min(n, (uint32_t)STAGES);
+            // A phase's blocks in order: weight tiles from w, in runs of `run`
+            // blocks that follow one another; seek(b) finds block b's tile and
+            // what is left of its run.  The token tiles, `xs_` of them in turn
+            // from `x`, exist once `bar` completes.
+            auto phase = [&](uint32_t b, uint32_t n, uint64_t *bar, auto seek, const uint8_t *x, uint32_t xs_) {
+                const uint32_t ahead = LOCAL ? n : min(n, (uint32_t)STAGES);
                 Loader<NT> lx = ld;
-                for (uint32_t i = 0; i < ahead; ++i, ++it, ld.next())
-                    if (!pipe_load<NT, false>(pipe, ld, w(b + i), NT * 128, p.err)) return false;
+                const uint8_t *w = nullptr;
+                uint32_t left = 0;
+                auto load = [&](uint32_t i) {
+                    if (left == 0) seek(b + i, w, left);
+                    if (!pipe_load<NT, LOCAL>(pipe, ld, w, LOCAL ? 0 : NT * 128, p.err)) return false;
+                    w += GLQ_FP8_TILE_BYTES;
+                    --left;
+                    ++it;
+                    ld.next();
+                    return true;
+                };
+                for (uint32_t i = 0; i < ahead; ++i)
+                    if (!load(i)) return false;
+                if (LOCAL) return true;
                 if (!pipe.wait(bar, 0, p.err)) return false;
                 fence_proxy_async();
+                uint32_t xi = b % xs_;
                 for (uint32_t i = 0; i < n; ++i) {
-                    if (i >= ahead) {
-                        if (!pipe_load<NT, false>(pipe, ld, w(b + i), NT * 128, p.err)) return false;
-                        ++it;
-                        ld.next();
-                    }
-                    bulk_g2s(lx.dst + GLQ_FP8_TILE_BYTES, x(b + i), NT * 128, &pipe.full[lx.stage]);
+                    if (i >= ahead && !load(i)) return false;
+                    bulk_g2s(lx.dst + GLQ_FP8_TILE_BYTES, x + (int64_t)xi * (NT * 128), NT * 128, &pipe.full[lx.stage]);
+                    if (++xi == xs_) xi = 0;
                     lx.next();
                 }
                 return true;
             };
+            // (an expert's gate and up tiles, and a row block of its down tiles,
+            // lie in the order of the blocks)
             const bool ok = phase(
                 b1, n1, &grid_bar[0],
-                [&](uint32_t b) {
-                    const uint32_t a = b / (R1 * KB1);
-                    return p.w13 + ((int64_t)list[a] * (R1 * KB1) + (b - a * (R1 * KB1))) * GLQ_FP8_TILE_BYTES;
+                [&](uint32_t b, const uint8_t *&w, uint32_t &left) {
+                    const uint32_t per = R1 * KB1, a = b / per, k = b - a * per;
+                    w = p.w13 + ((int64_t)list[a] * per + k) * GLQ_FP8_TILE_BYTES;
+                    left = per - k;
                 },
-                [&](uint32_t b) { return p.xq + (int64_t)(b % KB1) * (NT * 128); });
+                p.xq, KB1);
             if (ok)
                 phase(
                     b2, n2, &grid_bar[2],
-                    [&](uint32_t b) {
-                        const uint32_t rt = b / K2, k = b - rt * K2, a = k / IB;
-                        return p.w2 + (((int64_t)list[a] * DB + rt) * IB + (k - a * IB)) * GLQ_FP8_TILE_BYTES;
+                    [&](uint32_t b, const uint8_t *&w, uint32_t &left) {
+                        const uint32_t rt = b / K2, k = b - rt * K2, a = k / IB, ib = k - a * IB;
+                        w = p.w2 + (((int64_t)list[a] * DB + rt) * IB + ib) * GLQ_FP8_TILE_BYTES;
+                        left = IB - ib;
                     },
-                    [&](uint32_t b) { return p.hq + (int64_t)(b % K2) * (NT * 128); });
+                    p.hq, K2);
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -282,11 +323,11 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
     } else if (warp == GRID_WARP) {
         if (lane == 0) {
             uint64_t *const mine[4] = {nullptr, &part1, &formed, &part2};
-            for (int n = 0; n < 4; ++n) {
+            for (int n = LOCAL ? 1 : 0; n < 4; n += LOCAL ? 2 : 1) {
                 if (mine[n] && !pipe.wait(mine[n], 0, p.err)) break;
                 // release: what this CTA's warps wrote before they arrived
                 const uint64_t old = atom_add_u64(p.bar, 1);
-                const uint64_t target = (old / G + 1) * G;  // every call adds 4 G
+                const uint64_t target = (old / G + 1) * G;  // every call adds a multiple of G
                 const uint64_t t0 = sm100::clock_cycles();
                 bool ok = true;
                 while (ok && ld_acquire_u64(p.bar) < target) {
@@ -298,6 +339,24 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
             }
         }
     } else {
+        // One warp: four columns per lane of h of token t for expert a (its place
+        // among those in use; s = t K + which of t's choices), group ib.
+        auto expert_h = [&](uint32_t a, int s, int t, int ib, float (&h)[4]) {
+            float4 v[2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {  // gate, up
+                const uint32_t r = 2 * ib + g, first = (a * R1 + r) * KB1;
+                const int c0 = range_owner(first, total1, G1), c1 = range_owner(first + KB1 - 1, total1, G1);
+                v[g] = __ldcg(reinterpret_cast<const float4 *>(p.main + ((int64_t)s * R1 + r) * 128 + lane * 4));
+#pragma unroll 4
+                for (int c = c0 + 1; c <= c1; ++c)
+                    v[g] = add4(v[g], __ldcg(reinterpret_cast<const float4 *>(p.spill + ((int64_t)c * NT + t) * 128 + lane * 4)));
+            }
+            h[0] = silu(v[0].x) * v[1].x;
+            h[1] = silu(v[0].y) * v[1].y;
+            h[2] = silu(v[0].z) * v[1].z;
+            h[3] = silu(v[0].w) * v[1].w;
+        };
         // h^: a warp per (token, choice) and group of the expert's width
         auto form = [&]() {
             if (!pipe.wait_warp(&grid_bar[1], 0, p.err)) return false;
@@ -305,18 +364,8 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
                 const int s = i / (int)IB, ib = i - s * (int)IB, e = ids[s], t = s / K;
                 if (e < 0) continue;
                 const uint32_t a = rank[e];
-                float4 v[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {  // gate, up
-                    const uint32_t r = 2 * ib + h, first = (a * R1 + r) * KB1;
-                    const int c0 = range_owner(first, total1, G1), c1 = range_owner(first + KB1 - 1, total1, G1);
-                    v[h] = __ldcg(reinterpret_cast<const float4 *>(p.main + ((int64_t)s * R1 + r) * 128 + lane * 4));
-                    for (int c = c0 + 1; c <= c1; ++c)
-                        v[h] = add4(v[h], __ldcg(reinterpret_cast<const float4 *>(p.spill + ((int64_t)c * NT + t) * 128 + lane * 4)));
-                }
-                const float h[4] = {silu(v[0].x) * v[1].x, silu(v[0].y) * v[1].y, silu(v[0].z) * v[1].z,
-                                    silu(v[0].w) * v[1].w};
-                float sc;
+                float h[4], sc;
+                expert_h(a, s, t, ib, h);
                 const uint32_t q = warp_quantize(h, sc);
                 const int64_t tile = (int64_t)a * IB + ib;
                 __stcg(reinterpret_cast<uint32_t *>(p.hq + tile * (NT * 128) + sw128(t, lane >> 2)) + (lane & 3), q);
@@ -339,28 +388,75 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
                 pipe_x_done<NT, false>(pipe, i, lane);
                 return true;
             };
-            bool ok = pipe.wait_warp(&grid_bar[0], 0, p.err);
+            // the block scales come from DRAM, behind the weights in flight: into L2
+            // before those are too many
+            for (uint32_t j = (w0 * 32 + lane) * 32; j < n1; j += X_WARPS * 32 * 32) {
+                const uint32_t b = b1 + j, a = b / (R1 * KB1);
+                prefetch_l2(p.s13 + (int64_t)list[a] * (R1 * KB1) + (b - a * (R1 * KB1)));
+            }
+            for (uint32_t j = w0 * 32 + lane; j < n2; j += X_WARPS * 32) {
+                const uint32_t b = b2 + j, rt = b / K2, k = b - rt * K2, a = k / IB;
+                prefetch_l2(p.s2 + ((int64_t)list[a] * DB + rt) * IB + (k - a * IB));
+            }
+            bool ok = LOCAL || pipe.wait_warp(&grid_bar[0], 0, p.err);
             uint32_t i = w0;
             if (w0 >= turn) i = n1 + n2;
             for (; ok && i < n1; i += turn) {
                 const uint32_t b = b1 + i, a = b / (R1 * KB1), kb = b % KB1;
                 const float ws = __ldg(p.s13 + (int64_t)list[a] * (R1 * KB1) + (b - a * (R1 * KB1)));
-                float s[SC];
+                if constexpr (LOCAL) {
+                    const int col = kb * GLQ_FP8_BLOCK + lane * 4;
+                    uint2 w[LOCAL_T];
 #pragma unroll
-                for (int j = 0; j < SC; ++j) s[j] = j * 32 + lane < T ? __ldcg(p.xs + kb * NT + j * 32 + lane) * ws : 0.f;
-                ok = put(i, s);
-            }
-            ok = ok && form() && pipe.wait_warp(&grid_bar[2], 0, p.err);
-            for (; ok && i < n1 + n2; i += turn) {
-                const uint32_t b = b2 + (i - n1), rt = b / K2, k = b - rt * K2, a = k / IB;
-                const float ws = __ldg(p.s2 + ((int64_t)list[a] * DB + rt) * IB + (k - a * IB));
-                float s[SC];
+                    for (int t = 0; t < LOCAL_T; ++t) {
+                        w[t] = make_uint2(0, 0);
+                        if (t < T && col < p.d)
+                            w[t] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.d + col));
+                    }
+                    ok = p.x_dtype ? put_rounded<NT, __nv_bfloat16>(pipe, smem, i, w, T, ws, lane, p.err)
+                                   : put_rounded<NT, __half>(pipe, smem, i, w, T, ws, lane, p.err);
+                } else {
+                    float s[SC];
 #pragma unroll
-                for (int j = 0; j < SC; ++j) {
-                    const int t = j * 32 + lane;
-                    s[j] = t < T && slot[a * NT + t] != NONE ? __ldcg(p.hs + (int64_t)k * NT + t) * ws : 0.f;
+                    for (int j = 0; j < SC; ++j)
+                        s[j] = j * 32 + lane < T ? __ldcg(p.xs + kb * NT + j * 32 + lane) * ws : 0.f;
+                    ok = put(i, s);
                 }
-                ok = put(i, s);
+            }
+            if constexpr (LOCAL) ok = ok && pipe.wait_warp(&grid_bar[1], 0, p.err);
+            else ok = ok && form() && pipe.wait_warp(&grid_bar[2], 0, p.err);
+            for (; ok && i < n1 + n2; i += turn) {
+                const uint32_t b = b2 + (i - n1), rt = b / K2, k = b - rt * K2, a = k / IB, ib = k - a * IB;
+                const float ws = __ldg(p.s2 + ((int64_t)list[a] * DB + rt) * IB + ib);
+                float s[SC];
+                if constexpr (LOCAL) {
+                    uint32_t q[LOCAL_T];
+                    s[0] = 0.f;
+#pragma unroll
+                    for (int t = 0; t < LOCAL_T; ++t) {
+                        const uint8_t c = t < T ? slot[a * NT + t] : NONE;
+                        if (c == NONE) continue;
+                        float h[4], sc;
+                        expert_h(a, t * K + c, t, ib, h);
+                        q[t] = warp_quantize(h, sc);
+                        if (lane == t) s[0] = sc * wts[t * K + c] * ws;
+                    }
+                    if (!(ok = pipe_x_begin(pipe, i, p.err))) break;
+                    uint8_t *xt = pipe_x_tile<NT>(smem, i);
+#pragma unroll
+                    for (int t = 0; t < LOCAL_T; ++t)
+                        if (t < T && slot[a * NT + t] != NONE)
+                            *reinterpret_cast<uint32_t *>(xt + sw128(t, lane >> 2) + (lane & 3) * 4) = q[t];
+                    if (lane < NT) pipe.sc[i % STAGES][lane] = s[0];
+                    pipe_x_done<NT, true>(pipe, i, lane);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < SC; ++j) {
+                        const int t = j * 32 + lane;
+                        s[j] = t < T && slot[a * NT + t] != NONE ? __ldcg(p.hs + (int64_t)k * NT + t) * ws : 0.f;
+                    }
+                    ok = put(i, s);
+                }
             }
         } else {
             // ---------------- drain ----------------
@@ -398,7 +494,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
             }
             __syncwarp();
             if (ok && lane == 0) sm100::mbar_arrive(&part1);
-            ok = ok && form();
+            if (!LOCAL) ok = ok && form();
             // phase 2
             tile = b2 / K2;
             uint32_t k = b2 - tile * K2;
@@ -463,9 +559,9 @@ struct MoeKernel {
     int key;
 };
 
-template <int NT>
+template <int NT, bool LOCAL>
 MoeKernel moe_kernel_of(const MoeParams &p, int key) {
-    return {(const void *)moe_kernel<NT>,
+    return {(const void *)moe_kernel<NT, LOCAL>,
             1024 + layout_of(Pipe<NT>::STAGES * Pipe<NT>::STAGE_BYTES, NT, p.T, p.E, p.k).end, key};
 }
 
@@ -475,8 +571,11 @@ int moe_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
 cudaError_t launch_moe(const MoeParams &p, int grid, cudaStream_t s) {
     const int nt = moe_tile(p.T);
-    const MoeKernel k = nt == 16 ? moe_kernel_of<16>(p, 0) : nt == 32 ? moe_kernel_of<32>(p, 1) : moe_kernel_of<64>(p, 2);
-    static std::atomic<uint64_t> configured[3];
+    const MoeKernel k = p.T <= LOCAL_T ? moe_kernel_of<16, true>(p, 0)
+                        : nt == 16     ? moe_kernel_of<16, false>(p, 1)
+                        : nt == 32     ? moe_kernel_of<32, false>(p, 2)
+                                       : moe_kernel_of<64, false>(p, 3);
+    static std::atomic<uint64_t> configured[4];
     const cudaError_t e = once_per_device(configured[k.key], [&k] {
         return cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, MOE_SMEM_LIMIT);
     });
