@@ -342,15 +342,23 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
         // One warp: four columns per lane of h of token t for expert a (its place
         // among those in use; s = t K + which of t's choices), group ib.
         auto expert_h = [&](uint32_t a, int s, int t, int ib, float (&h)[4]) {
-            float4 v[2];
+            float4 v[2], more[2];
+            int c0[2], c1[2];
+            const float *spill = p.spill + (int64_t)t * 128 + lane * 4;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {  // gate, up
+            for (int g = 0; g < 2; ++g) {  // gate, up: every load before the first sum
                 const uint32_t r = 2 * ib + g, first = (a * R1 + r) * KB1;
-                const int c0 = range_owner(first, total1, G1), c1 = range_owner(first + KB1 - 1, total1, G1);
+                c0[g] = range_owner(first, total1, G1), c1[g] = range_owner(first + KB1 - 1, total1, G1);
                 v[g] = __ldcg(reinterpret_cast<const float4 *>(p.main + ((int64_t)s * R1 + r) * 128 + lane * 4));
+                more[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c1[g] > c0[g]) more[g] = __ldcg(reinterpret_cast<const float4 *>(spill + (int64_t)(c0[g] + 1) * NT * 128));
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                v[g] = add4(v[g], more[g]);
 #pragma unroll 4
-                for (int c = c0 + 1; c <= c1; ++c)
-                    v[g] = add4(v[g], __ldcg(reinterpret_cast<const float4 *>(p.spill + ((int64_t)c * NT + t) * 128 + lane * 4)));
+                for (int c = c0[g] + 2; c <= c1[g]; ++c)
+                    v[g] = add4(v[g], __ldcg(reinterpret_cast<const float4 *>(spill + (int64_t)c * NT * 128)));
             }
             h[0] = silu(v[0].x) * v[1].x;
             h[1] = silu(v[0].y) * v[1].y;
@@ -430,23 +438,18 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
                 const float ws = __ldg(p.s2 + ((int64_t)list[a] * DB + rt) * IB + ib);
                 float s[SC];
                 if constexpr (LOCAL) {
-                    uint32_t q[LOCAL_T];
+                    if (!(ok = pipe_x_begin(pipe, i, p.err))) break;
+                    uint8_t *xt = pipe_x_tile<NT>(smem, i);
                     s[0] = 0.f;
-#pragma unroll
-                    for (int t = 0; t < LOCAL_T; ++t) {
-                        const uint8_t c = t < T ? slot[a * NT + t] : NONE;
+#pragma unroll 1
+                    for (int t = 0; t < T; ++t) {  // rolled: it runs a few times a call, from a cold instruction cache
+                        const uint8_t c = slot[a * NT + t];
                         if (c == NONE) continue;
                         float h[4], sc;
                         expert_h(a, t * K + c, t, ib, h);
-                        q[t] = warp_quantize(h, sc);
+                        *reinterpret_cast<uint32_t *>(xt + sw128(t, lane >> 2) + (lane & 3) * 4) = warp_quantize(h, sc);
                         if (lane == t) s[0] = sc * wts[t * K + c] * ws;
                     }
-                    if (!(ok = pipe_x_begin(pipe, i, p.err))) break;
-                    uint8_t *xt = pipe_x_tile<NT>(smem, i);
-#pragma unroll
-                    for (int t = 0; t < LOCAL_T; ++t)
-                        if (t < T && slot[a * NT + t] != NONE)
-                            *reinterpret_cast<uint32_t *>(xt + sw128(t, lane >> 2) + (lane & 3) * 4) = q[t];
                     if (lane < NT) pipe.sc[i % STAGES][lane] = s[0];
                     pipe_x_done<NT, true>(pipe, i, lane);
                 } else {
@@ -465,64 +468,53 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
             float acc[HALF];
             uint32_t i = 0;
             bool ok = true;
-            // phase 1: sums per (token, expert); the piece with a tile's first
-            // block in `main`, a CTA's piece of an earlier CTA's tile in `spill`
-            uint32_t tile = b1 / KB1, kb = b1 - tile * KB1;
-            while (ok && i < n1) {
-                const uint32_t len = min(KB1 - kb, n1 - i);
+            // Phase 0: sums per (token, expert); the piece with a tile's first block
+            // in `main`, a CTA's piece of an earlier CTA's tile in `spill`.  Phase
+            // 1: sums per token; a CTA's piece of a split tile in `part`.
+            auto phase = [&](auto skip, int ph) {
+                constexpr bool SKIP = decltype(skip)::value;
+                const uint32_t end = ph ? n1 + n2 : n1, KT = ph ? K2 : KB1, b = ph ? b2 : b1;
+                uint32_t tile = b / KT, k = b - tile * KT;
+                while (ok && i < end) {
+                    const uint32_t len = min(KT - k, end - i);
 #pragma unroll
-                for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
-                for (uint32_t n = 0; ok && n < len;) {
-                    const bool two = DRAIN == 2 && n + 2 <= len;
-                    ok = two ? pipe_drain<NT, DRAIN, false>(pipe, i, quadrant, set, acc, p.err)
-                             : pipe_drain<NT, 1, false>(pipe, i, quadrant, set, acc, p.err);
-                    n += two ? 2 : 1;
-                    i += two ? 2 : 1;
-                }
-                if (!ok) break;
-                const uint32_t a = tile / R1, r = tile - a * R1;
+                    for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
+                    for (uint32_t n = 0; ok && n < len;) {
+                        const bool two = DRAIN == 2 && n + 2 <= len;
+                        ok = two ? pipe_drain<NT, DRAIN, SKIP>(pipe, i, quadrant, set, acc, p.err)
+                                 : pipe_drain<NT, 1, SKIP>(pipe, i, quadrant, set, acc, p.err);
+                        n += two ? 2 : 1;
+                        i += two ? 2 : 1;
+                    }
+                    if (!ok) break;
+                    const uint32_t a = tile / R1, r = tile - a * R1;   // phase 0
+                    const bool whole = k == 0 && len == KT;            // phase 1
+                    const int64_t col = (int64_t)tile * 128 + row;
+                    float *part = p.part + ((int64_t)cta * 2 + (k == 0 ? 1 : 0)) * NT * 128 + row;
 #pragma unroll
-                for (int j = 0; j < HALF; ++j) {
-                    const int t = set * HALF + j;
-                    const uint8_t c = slot[a * NT + t];
-                    if (c == NONE) continue;
-                    __stcg(kb == 0 ? p.main + (((int64_t)t * K + c) * R1 + r) * 128 + row
-                                   : p.spill + ((int64_t)cta * NT + t) * 128 + row, acc[j]);
+                    for (int j = 0; j < HALF; ++j) {
+                        const int t = set * HALF + j;
+                        if (t >= T) continue;
+                        if (ph == 0) {
+                            const uint8_t c = slot[a * NT + t];
+                            if (c != NONE)
+                                __stcg(k == 0 ? p.main + (((int64_t)t * K + c) * R1 + r) * 128 + row
+                                              : p.spill + ((int64_t)cta * NT + t) * 128 + row, acc[j]);
+                        } else if (!whole) {
+                            __stcg(part + t * 128, acc[j]);
+                        } else if (col < p.d) {
+                            store_y(p.y, p.y_dtype, (int64_t)t * p.d + col, acc[j]);
+                        }
+                    }
+                    ++tile;
+                    k = 0;
                 }
-                ++tile;
-                kb = 0;
-            }
+            };
+            phase(std::false_type{}, 0);
             __syncwarp();
             if (ok && lane == 0) sm100::mbar_arrive(&part1);
             if (!LOCAL) ok = ok && form();
-            // phase 2
-            tile = b2 / K2;
-            uint32_t k = b2 - tile * K2;
-            while (ok && i < n1 + n2) {
-                const uint32_t len = min(K2 - k, n1 + n2 - i);
-#pragma unroll
-                for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
-                for (uint32_t n = 0; ok && n < len;) {
-                    const bool two = DRAIN == 2 && n + 2 <= len;
-                    ok = two ? pipe_drain<NT, DRAIN, true>(pipe, i, quadrant, set, acc, p.err)
-                             : pipe_drain<NT, 1, true>(pipe, i, quadrant, set, acc, p.err);
-                    n += two ? 2 : 1;
-                    i += two ? 2 : 1;
-                }
-                if (!ok) break;
-                const bool whole = k == 0 && len == K2;
-                const int64_t col = (int64_t)tile * 128 + row;
-                float *part = p.part + ((int64_t)cta * 2 + (k == 0 ? 1 : 0)) * NT * 128 + row;
-#pragma unroll
-                for (int j = 0; j < HALF; ++j) {
-                    const int t = set * HALF + j;
-                    if (t >= T) continue;
-                    if (!whole) __stcg(part + t * 128, acc[j]);
-                    else if (col < p.d) store_y(p.y, p.y_dtype, (int64_t)t * p.d + col, acc[j]);
-                }
-                ++tile;
-                k = 0;
-            }
+            phase(std::true_type{}, 1);
             __syncwarp();
             if (ok && lane == 0) sm100::mbar_arrive(&part2);
             ok = ok && pipe.wait_warp(&grid_bar[3], 0, p.err);
