@@ -16,6 +16,7 @@ no CPU fallback: if the library is missing, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -590,6 +591,8 @@ class GlqLinear:
 
 FP8_BLOCK = 128
 _DTYPE_CODES = {}  # torch dtype -> code, as they are met
+_E4M3_F32 = None
+_HERE_ALREADY = contextlib.nullcontext()
 
 
 
@@ -597,15 +600,35 @@ def _fp8_blocks(v: int) -> int:
     return -(-v // FP8_BLOCK)
 
 
+_raw_stream = None  # torch's raw handle of a device's current stream, bound by the first call
+
+
 def _call_stream(index, stream, *tensors):
     """The raw stream of a call on device `index`; tensors used on a stream
     that is not their allocator's current one are recorded there."""
-    current = _torch()._C._cuda_getCurrentRawStream(index)
+    global _raw_stream
+    if _raw_stream is None:
+        _raw_stream = _torch()._C._cuda_getCurrentRawStream
+    current = _raw_stream(index)
     if stream is None or stream.cuda_stream == current:
         return current
     for t in tensors:
         t.record_stream(stream)
     return stream.cuda_stream
+
+
+def _fp8_dtypes():
+    global _E4M3_F32
+    if _E4M3_F32 is None:
+        torch = _torch()
+        _E4M3_F32 = (torch.float8_e4m3fn, torch.float32)
+    return _E4M3_F32
+
+
+def _on_device(index):
+    """Makes `index` the current device, if it is not."""
+    torch = _torch()
+    return _HERE_ALREADY if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
 
 def _dtype_code(t):
@@ -650,26 +673,23 @@ def fp8_quantize(x, q=None, s=None, stream=None):
     scale per token and group of 128 columns: (q [B][G * 128], s [G][B]), G =
     ceil(n / 128), columns of q from n zero.  Several Fp8Linear layers can
     then take them (forward_quantized).  Definition: glq_fp8_quantize."""
-    torch = _torch()
     _check_input("x", x, None)
-    (B, n), index = x.shape, x.get_device()
+    B, n, index = x.size(0), x.size(1), x.get_device()
+    e4m3, f32 = _fp8_dtypes()
     G = _fp8_blocks(n)
     if q is None:
-        q = torch.empty((B, G * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
+        q = x.new_empty((B, G * FP8_BLOCK), dtype=e4m3)
     else:
         _check_output("q", q, (B, G * FP8_BLOCK), index)
     if s is None:
-        s = torch.empty((G, B), dtype=torch.float32, device=x.device)
+        s = x.new_empty((G, B), dtype=f32)
     else:
         _check_output("s", s, (G, B), index)
-    if q.dtype != torch.float8_e4m3fn or s.dtype != torch.float32:
+    if q.dtype != e4m3 or s.dtype != f32:
         raise ValueError("q must be float8_e4m3fn and s float32")
     args = (x.data_ptr(), _dtype_code(x), B, n, q.data_ptr(), s.data_ptr(), _call_stream(index, stream, x, q, s))
-    if index == torch.cuda.current_device():
+    with _on_device(index):
         glq_fp8_quantize(*args)
-    else:
-        with torch.cuda.device(index):
-            glq_fp8_quantize(*args)
     return q, s
 
 

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256) fp8_dequant_kernel(const uint8_t *tiles, 
 
 // ---------------------------------------------------------------------------
 // Few tokens.  Reads every weight once: bound by HBM for small batches.  An
-// output tile is 128 weight rows x NT tokens; a cluster of C CTAs (one per SM)
+// output tile is 128 weight rows x all tokens; a cluster of C CTAs (one per SM)
 // takes tile after tile, each CTA 1 / C of its K blocks, so that few tiles
 // still keep most SMs loading.  The parts meet in distributed shared memory:
 // token j is summed by CTA j mod C of the cluster, in the order of the CTAs.
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t C = p.C, rank = C > 1 ? sm100::cluster_ctarank() : 0;
-    const uint32_t NC = gridDim.x / C, TT = p.TT, tiles = p.RT * TT;
+    const uint32_t NC = gridDim.x / C, tiles = p.RT;
     // this CTA's K blocks of every tile
     const uint32_t k0 = rank * p.KB / C, nk = (rank + 1) * p.KB / C - k0;
     const uint32_t first = blockIdx.x / C;
@@ -167,33 +167,32 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
         if (elect_one()) {
             copier = true;
             Loader<NT> ld(smem);
-            // weights are constant: the first copies do not wait for the kernel
-            // before, which the rounded tokens come from
-            const uint32_t ahead = ROUND ? 0 : min(nblk, (uint32_t)STAGES);
-            for (uint32_t t = first; t < tiles && it < ahead; t += NC) {
-                const uint8_t *w = p.w + ((int64_t)(t / TT) * p.KB + k0) * GLQ_FP8_TILE_BYTES;
-                for (uint32_t k = 0; k < nk && it < ahead; ++k, ++it, w += GLQ_FP8_TILE_BYTES, ld.next())
-                    pipe_load<NT, ROUND>(pipe, ld, w, NT * 128, p.err);
-            }
-            if (!ROUND) {
+            uint32_t ahead = 0;
+            if constexpr (!ROUND) {
+                // weights are constant: the first copies do not wait for the
+                // kernel before, which the rounded tokens come from
+                ahead = min(nblk, (uint32_t)STAGES);
+                for (uint32_t t = first; t < tiles && it < ahead; t += NC) {
+                    const uint8_t *w = p.w + ((int64_t)t * p.KB + k0) * GLQ_FP8_TILE_BYTES;
+                    for (uint32_t k = 0; k < nk && it < ahead; ++k, ++it, w += GLQ_FP8_TILE_BYTES, ld.next())
+                        pipe_load<NT, ROUND>(pipe, ld, w, NT * 128, p.err);
+                }
                 sm100::prefetch_tensormap(&qmap);
                 pdl_wait();
+                ld = Loader<NT>(smem);
             }
             uint32_t i = 0;
             bool ok = true;
-            ld = Loader<NT>(smem);
             for (uint32_t t = first; t < tiles && ok; t += NC) {
-                const uint32_t rt = t / TT;
-                const uint8_t *w = p.w + ((int64_t)rt * p.KB + k0) * GLQ_FP8_TILE_BYTES;
-                const int tok0 = (int)(t - rt * TT) * NT;
+                const uint8_t *w = p.w + ((int64_t)t * p.KB + k0) * GLQ_FP8_TILE_BYTES;
                 int col = (int)k0 * GLQ_FP8_BLOCK;
                 for (uint32_t k = 0; k < nk; ++k, ++i, w += GLQ_FP8_TILE_BYTES, col += GLQ_FP8_BLOCK, ld.next()) {
-                    if (i >= ahead) {
+                    if (ROUND || i >= ahead) {
                         ok = pipe_load<NT, ROUND>(pipe, ld, w, ROUND ? 0 : NT * 128, p.err);
                         if (!ok) break;
                         ++it;
                     }
-                    if (!ROUND) sm100::tma_load_2d(ld.dst + GLQ_FP8_TILE_BYTES, &qmap, &pipe.full[ld.stage], col, tok0);
+                    if (!ROUND) sm100::tma_load_2d(ld.dst + GLQ_FP8_TILE_BYTES, &qmap, &pipe.full[ld.stage], col, 0);
                 }
             }
         }
@@ -207,7 +206,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
         // the block scales of this CTA come from DRAM, behind the weights in
         // flight: into L2 before those are too many
         for (uint32_t t = first + (warp - X_WARP0) * NC; t < tiles; t += X_WARPS * NC)
-            for (uint32_t k = lane * 32; k < nk; k += 32 * 32) prefetch_l2(p.ws + (int64_t)(t / TT) * p.KB + k0 + k);
+            for (uint32_t k = lane * 32; k < nk; k += 32 * 32) prefetch_l2(p.ws + (int64_t)t * p.KB + k0 + k);
         pdl_wait();
         // Everything a block needs from memory is loaded one turn ahead (the
         // block scales come from DRAM, behind the weights in flight) and
@@ -223,23 +222,22 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
         const uint32_t turn = Pipe<NT>::X_TURN;
         auto fetch = [&](uint32_t i, Ahead &f) {
             if (i >= nblk) return;
-            const uint32_t q = i / nk, t = first + q * NC, k = k0 + (i - q * nk), rt = t / TT;
-            const int tok0 = (int)(t - rt * TT) * NT, live = min(NT, p.B - tok0);
-            f.ws = __ldg(p.ws + (int64_t)rt * p.KB + k);
-            if constexpr (ROUND) {  // TT is 1
+            const uint32_t q = i / nk, k = k0 + (i - q * nk);
+            f.ws = __ldg(p.ws + (int64_t)(first + q * NC) * p.KB + k);
+            if constexpr (ROUND) {
                 const int col = k * GLQ_FP8_BLOCK + lane * 4;
                 const T *src = static_cast<const T *>(p.x) + col;
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) {
                     f.x[r] = make_uint2(0, 0);
                     // n is a multiple of 8: a lane's four columns are in or out together
-                    if (r < live && col < p.n) f.x[r] = __ldg(reinterpret_cast<const uint2 *>(src + (int64_t)r * p.n));
+                    if (r < p.B && col < p.n) f.x[r] = __ldg(reinterpret_cast<const uint2 *>(src + (int64_t)r * p.n));
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < SC; ++j) {
                     const int tok = j * 32 + lane;
-                    f.s[j] = tok < live ? p.s[(int64_t)k * p.s_ld + tok0 + tok] : 0.f;
+                    f.s[j] = tok < p.B ? p.s[(int64_t)k * p.s_ld + tok] : 0.f;
                 }
             }
         };
@@ -280,7 +278,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
         float acc[HALF];
         uint32_t i = 0, round = 0;
         for (uint32_t t = first; t < tiles; t += NC, ++round) {
-            const int rt = (int)(t / TT), tok0 = (int)(t - rt * TT) * NT, live = min(NT, p.B - tok0);
+            const int live = p.B;
 #pragma unroll
             for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
             bool ok = true;
@@ -293,12 +291,12 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
             }
             if (!ok) break;
             if (C == 1) {
-                const int row = rt * 128 + row_l;
+                const int row = t * 128 + row_l;
                 if (row < p.m) {
 #pragma unroll
                     for (int j = 0; j < HALF; ++j)
                         if (set * HALF + j < live)
-                            store_y(p.y, p.y_dtype, (int64_t)(tok0 + set * HALF + j) * p.m + row, acc[j]);
+                            store_y(p.y, p.y_dtype, (int64_t)(set * HALF + j) * p.m + row, acc[j]);
                 }
                 continue;
             }
@@ -316,7 +314,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
             }
             if (!pipe.wait_warp(&pipe.red_full, round & 1, p.err)) break;
             // a warp sums one token in eight, a lane four rows
-            const int row = rt * 128 + lane * 4;
+            const int row = t * 128 + lane * 4;
             for (int own = dtid >> 5; own < mine; own += D_WARPS) {
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (uint32_t c = 0; c < C; ++c) {
@@ -324,7 +322,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
                     sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
                 }
                 // m is a multiple of 8: four rows are in or out together
-                if (row < p.m) store_y4(p.y, p.y_dtype, (int64_t)(tok0 + own * (int)C + (int)rank) * p.m + row, sum);
+                if (row < p.m) store_y4(p.y, p.y_dtype, (int64_t)(own * (int)C + (int)rank) * p.m + row, sum);
             }
             __syncwarp();
             // in the last round nobody waits for it, and a CTA may leave as soon
@@ -372,7 +370,7 @@ cudaError_t launch_fp8_dequant(const uint8_t *tiles, const float *scale, float *
     return cudaGetLastError();
 }
 
-int fp8_skinny_tile(int64_t B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : 128; }
+int fp8_skinny_tile(int64_t B) { return B <= 16 ? 16 : B <= 32 ? 32 : 64; }
 
 namespace {
 
@@ -389,14 +387,13 @@ SkinnyKernel skinny_kernel(int source, int nt) {
     switch (nt) {
         case 16: return {(const void *)fp8_skinny_kernel<16, 2>, Pipe<16>::SMEM_BYTES, 2};
         case 32: return {(const void *)fp8_skinny_kernel<32, 2>, Pipe<32>::SMEM_BYTES, 3};
-        case 64: return {(const void *)fp8_skinny_kernel<64, 2>, Pipe<64>::SMEM_BYTES, 4};
-        default: return {(const void *)fp8_skinny_kernel<128, 2>, Pipe<128>::SMEM_BYTES, 5};
+        default: return {(const void *)fp8_skinny_kernel<64, 2>, Pipe<64>::SMEM_BYTES, 4};
     }
 }
 
 // Sets the kernel's shared memory limit once per device.
 cudaError_t prepare(const SkinnyKernel &k) {
-    static std::atomic<uint64_t> configured[6];
+    static std::atomic<uint64_t> configured[5];
     return once_per_device(configured[k.key], [&k] {
         return cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
     });

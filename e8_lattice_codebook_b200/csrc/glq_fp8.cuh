@@ -216,8 +216,8 @@ constexpr int D_THREADS = D_WARPS * 32;
 template <int NT>
 struct Pipe {
     static constexpr int STAGE_BYTES = GLQ_FP8_TILE_BYTES + NT * 128;
-    // as many as shared memory holds beside the parts buffer, or as TMEM does (128 tokens)
-    static constexpr int STAGES = NT == 16 ? 11 : NT == 32 ? 9 : NT == 64 ? 7 : 4;
+    // as many as shared memory holds beside the parts buffer
+    static constexpr int STAGES = NT == 16 ? 11 : NT == 32 ? 9 : 7;
     static constexpr int TMEM_COLS = NT == 16 ? 256 : 512;
     static_assert(STAGES * NT <= TMEM_COLS, "a slot per stage");
     static constexpr int HALF = NT / 2;     // tokens of one drain set

@@ -53,7 +53,8 @@ cudaError_t launch_fp8_pack(const Fp8PackParams &p, cudaStream_t s);
 cudaError_t launch_fp8_dequant(const uint8_t *tiles, const float *scale, float *w, int m, int n, int KB,
                                cudaStream_t s);
 
-// y [B][m] = x W^T on 128-row x NT-token tiles, clusters of C CTAs splitting K
+// y [B][m] = x W^T for B <= NT tokens, tiles of 128 rows, clusters of C CTAs
+// splitting K
 struct Fp8SkinnyParams {
     const uint8_t *w;
     const float *ws;
@@ -62,12 +63,13 @@ struct Fp8SkinnyParams {
     int64_t s_ld;
     void *y;
     int y_dtype;
-    int m, n, B, RT, KB, TT;  // TT token tiles
+    int m, n, B, RT, KB;
     int C;              // CTAs per cluster, 1..8, at most KB
     unsigned *err;
 };
 constexpr int FP8_ROUND_MAX = 4;  // most tokens of sources 0 and 1
-int fp8_skinny_tile(int64_t B);  // NT: tokens per tile for a batch of B
+constexpr int FP8_FEW = 64;       // most tokens of the few-token kernel
+int fp8_skinny_tile(int64_t B);  // NT: tokens per tile for a batch of B <= FP8_FEW
 // clusters of c = 1..8 CTAs (one per SM) the current device holds at once
 cudaError_t fp8_skinny_clusters(int num_sms, int count[9]);
 struct Fp8SkinnyPlan {
@@ -84,12 +86,19 @@ struct Fp8GemmParams {
     const float *ws;
     const float *s;     // [KB][s_ld]
     int64_t s_ld;
-    void *y;
-    int y_dtype;
+    int y_dtype;        // of ymap
     int m, B, RT, KB;
     int TT, tiles;      // token tiles; all tiles, token tiles within a column of them
+    int ksplit;         // parts of K; with more than one, ymap is the fp32 parts,
+    int part_rows;      // this many rows apart
     unsigned *err;
 };
+// the parts of K for a layer and batch (host only)
+int plan_fp8_gemm(int64_t tiles, int KB, int64_t B, int64_t m, int num_sms);
+// y (count values, a multiple of 4) = the sum of `parts` arrays part_stride
+// floats apart
+cudaError_t launch_fp8_sum_parts(const float *part, int64_t part_stride, int parts, void *y, int y_dtype, int64_t count,
+                                 cudaStream_t s, bool pdl);
 // qmap: boxes of 128 columns x 128 tokens of q, 128-byte swizzle; wmap: the
 // laid-out weights as rows of 128 bytes, boxes of 64 rows, no swizzle; ymap:
 // boxes of 128 bytes x 32 tokens of y, 128-byte swizzle

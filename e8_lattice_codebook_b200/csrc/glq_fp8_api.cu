@@ -79,12 +79,31 @@ void free_fp8(glq_fp8 L) {
 // their own rounds them first.
 bool rounds_inside(int64_t B) { return B <= glq::FP8_ROUND_MAX; }
 
-// Batches for the many-token kernel.
-bool many_tokens(int64_t B) { return B > 64; }
+// The many-token kernel's tiles and parts of K.
+glq::Fp8GemmParams gemm_params(glq_fp8 L, int64_t B) {
+    glq::Fp8GemmParams p{};
+    p.ws = L->d_ws;
+    p.m = (int)L->m;
+    p.B = (int)B;
+    p.RT = L->RT;
+    p.KB = L->KB;
+    p.TT = (int)((B + glq::FP8_GEMM_TOK - 1) / glq::FP8_GEMM_TOK);
+    p.tiles = (L->RT + 1) / 2 * p.TT;
+    p.ksplit = glq::plan_fp8_gemm(p.tiles, p.KB, B, L->m, L->num_sms);
+    p.part_rows = (int)((B + 31) / 32 * 32);  // stores come in boxes of 32 rows
+    p.err = L->d_err;
+    return p;
+}
 
 // What a call of B tokens needs of the shared workspace.
 void fp8_need(glq_fp8 L, int64_t B, bool quantized, size_t need[glq::FP8_WS_COUNT]) {
     B = std::min(B, MAX_SLICE);
+    if (B > glq::FP8_FEW) {
+        const glq::Fp8GemmParams p = gemm_params(L, B);
+        if (p.ksplit > 1)
+            need[glq::FP8_WS_Z] =
+                std::max(need[glq::FP8_WS_Z], (size_t)p.ksplit * p.part_rows * (size_t)L->m * sizeof(float));
+    }
     if (B <= 0 || quantized || rounds_inside(B)) return;
     need[glq::FP8_WS_Q] = std::max(need[glq::FP8_WS_Q], (size_t)B * L->KB * GLQ_FP8_BLOCK);
     need[glq::FP8_WS_S] = std::max(need[glq::FP8_WS_S], (size_t)B * L->KB * sizeof(float));
@@ -98,7 +117,6 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
     void *buf[glq::FP8_WS_COUNT];
     const glq_status ok = glq::fp8_workspace(L->device, need, st, buf);
     if (ok != GLQ_OK) return ok;
-    const int nt = glq::fp8_skinny_tile(B);
     int source = 2;
     if (!q && rounds_inside(B)) source = x_dtype;
     if (!q && source == 2) {
@@ -115,28 +133,25 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
         s = p.s;
         s_ld = B;
     }
-    if (many_tokens(B)) {
-        glq::Fp8GemmParams p{};
-        p.ws = L->d_ws;
+    if (B > glq::FP8_FEW) {
+        glq::Fp8GemmParams p = gemm_params(L, B);
+        const bool split = p.ksplit > 1;
+        void *z = split ? buf[glq::FP8_WS_Z] : y;
         p.s = s;
         p.s_ld = s_ld;
-        p.y = y;
-        p.y_dtype = y_dtype;
-        p.m = (int)L->m;
-        p.B = (int)B;
-        p.RT = L->RT;
-        p.KB = L->KB;
-        p.TT = (int)((B + glq::FP8_GEMM_TOK - 1) / glq::FP8_GEMM_TOK);
-        p.tiles = (L->RT + 1) / 2 * p.TT;
-        p.err = L->d_err;
+        p.y_dtype = split ? GLQ_F32 : y_dtype;
         CUtensorMap qmap, wmap, ymap;
         if (!encode_e4m3(&qmap, q, (int64_t)L->KB * GLQ_FP8_BLOCK, B, 128) ||
             !encode_e4m3(&wmap, L->d_w, GLQ_FP8_BLOCK, (int64_t)L->RT * L->KB * 128, 64, false) ||
-            !encode_rows(&ymap, y_dtype == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
-                         y_dtype == 2 ? 4 : 2, y, L->m, B, 32))
+            !encode_rows(&ymap, p.y_dtype == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                         p.y_dtype == 2 ? 4 : 2, z, L->m, split ? (int64_t)p.ksplit * p.part_rows : B, 32))
             return GLQ_ERR_CUDA;
-        return launched(glq::launch_fp8_gemm(p, qmap, wmap, ymap, L->num_sms, st, true));
+        const glq_status e = launched(glq::launch_fp8_gemm(p, qmap, wmap, ymap, L->num_sms, st, true));
+        if (e != GLQ_OK || !split) return e;
+        return launched(glq::launch_fp8_sum_parts(static_cast<float *>(z), (int64_t)p.part_rows * L->m, p.ksplit, y,
+                                                  y_dtype, B * L->m, st, true));
     }
+    const int nt = glq::fp8_skinny_tile(B);
     glq::Fp8SkinnyParams p{};
     p.w = L->d_w;
     p.ws = L->d_ws;
@@ -150,9 +165,8 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
     p.B = (int)B;
     p.RT = L->RT;
     p.KB = L->KB;
-    p.TT = (int)((B + nt - 1) / nt);
     p.err = L->d_err;
-    const glq::Fp8SkinnyPlan plan = glq::plan_fp8_skinny((int64_t)p.RT * p.TT, p.KB, L->clusters);
+    const glq::Fp8SkinnyPlan plan = glq::plan_fp8_skinny(p.RT, p.KB, L->clusters);
     p.C = plan.C;
     CUtensorMap qmap{};
     if (source == 2 && !encode_e4m3(&qmap, q, (int64_t)L->KB * GLQ_FP8_BLOCK, B, nt)) return GLQ_ERR_CUDA;
@@ -320,7 +334,8 @@ glq_status glq_fp8_reserve(glq_fp8 layer, int64_t max_B) {
     if (max_B < 0) return GLQ_ERR_SHAPE;
     DeviceGuard guard(layer->device);
     size_t need[glq::FP8_WS_COUNT] = {};
-    fp8_need(layer, max_B, false, need);
+    // every batch up to max_B: the parts of K depend on it
+    for (int64_t B = 1; B <= std::min(max_B, MAX_SLICE); ++B) fp8_need(layer, B, false, need);
     void *buf[glq::FP8_WS_COUNT];
     return glq::fp8_workspace(layer->device, need, 0, buf);
 }

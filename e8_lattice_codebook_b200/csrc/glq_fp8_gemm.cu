@@ -132,7 +132,21 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
     // tcgen05 fences), no stores of another CTA.  Cluster-scope acquires, one
     // per drain warp and K block, cost more than the K block's MMAs.
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bounded(bar, parity, &abort_flag, p.err); };
-    const int KB = p.KB;
+    const int KB = p.KB, items = p.tiles * p.ksplit;
+    // an item: a tile's token and weight-row place and its share of the K blocks
+    struct Item {
+        int ct, tt, ks, kb0, kb1;
+    };
+    auto item = [&](int i) {
+        Item w;
+        const int tile = i / p.ksplit;
+        w.ks = i - tile * p.ksplit;
+        w.ct = tile / p.TT;
+        w.tt = tile - w.ct * p.TT;
+        w.kb0 = w.ks * KB / p.ksplit;
+        w.kb1 = (w.ks + 1) * KB / p.ksplit;
+        return w;
+    };
 
     if (warp < DRAIN_WARP0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -141,13 +155,13 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
             pdl_wait();  // the rounded tokens come from the kernel before
             uint32_t s = 0, par = 1, loaded = 0;
             bool ok = true;
-            for (int tile = cid; tile < p.tiles && ok; tile += ncl) {
-                const int ct = tile / p.TT, tt = tile - ct * p.TT;
-                const int tok0 = tt * (2 * TOK) + (int)rank * TOK;
+            for (int it = cid; it < items && ok; it += ncl) {
+                const Item w = item(it);
+                const int ct = w.ct, tok0 = w.tt * (2 * TOK) + (int)rank * TOK;
                 const bool both = 2 * ct + 1 < p.RT;             // the second block of weight rows exists
                 const uint32_t bytes = 2 * (A_BYTES + (both ? 2 : 1) * B_BYTES);
-                int wrow = 2 * ct * KB * 128 + (int)rank * 64;   // this CTA's 64 rows of a block
-                for (int kb = 0; kb < KB; ++kb, wrow += 128) {
+                int wrow = (2 * ct * KB + w.kb0) * 128 + (int)rank * 64;  // this CTA's 64 rows of a block
+                for (int kb = w.kb0; kb < w.kb1; ++kb, wrow += 128) {
                     if (!(ok = wait(&empty[s], par))) break;
                     uint8_t *st = smem + s * STAGE;
                     if (rank == 0) mbar_expect_tx(&full[s], bytes);
@@ -168,8 +182,9 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
                 const uint32_t idesc = idesc_e4m3_f32(2 * TOK, COLS);
                 uint32_t s = 0, par = 0, a = 0, apar = 1;
                 bool ok = true;
-                for (int tile = cid; tile < p.tiles && ok; tile += ncl) {
-                    for (int kb = 0; kb < KB; ++kb) {
+                for (int it = cid; it < items && ok; it += ncl) {
+                    const Item w = item(it);
+                    for (int kb = w.kb0; kb < w.kb1; ++kb) {
                         if (!(ok = wait(&full[s], par))) break;
                         uint8_t *st = smem + s * STAGE;
                         const uint64_t ad = sm100::smem_desc_sw128(st);
@@ -203,10 +218,10 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
         const uint32_t t0 = tmem + ((uint32_t)(32 * quadrant) << 16) + half * 2 * COLS;
         uint32_t a = 0, apar = 0;
         bool ok = true;
-        for (int tile = cid; tile < p.tiles && ok; tile += ncl) {
-            const int ct = tile / p.TT, tt = tile - ct * p.TT;
-            const int token = tt * (2 * TOK) + (int)rank * TOK + 32 * quadrant + lane;
-            const int rt = 2 * ct + half;
+        for (int it = cid; it < items && ok; it += ncl) {
+            const Item w = item(it);
+            const int token = w.tt * (2 * TOK) + (int)rank * TOK + 32 * quadrant + lane;
+            const int rt = 2 * w.ct + half;
             const float *s = p.s + min(token, p.B - 1);
             const float *ws = p.ws + (int64_t)min(rt, p.RT - 1) * KB;
             float acc[128];
@@ -219,19 +234,19 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
             auto fetch = [&](int kb0) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int kb = min(kb0 + i, KB - 1);
+                    const int kb = min(kb0 + i, w.kb1 - 1);
                     rs[i] = __ldg(s + (int64_t)kb * p.s_ld);
                     rw[i] = __ldg(ws + kb);
                 }
             };
-            fetch(0);
-            for (int kb0 = 0; kb0 < KB && ok; kb0 += 4) {
+            fetch(w.kb0);
+            for (int kb0 = w.kb0; kb0 < w.kb1 && ok; kb0 += 4) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[i] = rs[i] * rw[i];
                 fetch(kb0 + 4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (kb0 + i >= KB) break;
+                    if (kb0 + i >= w.kb1) break;
                     if (lane == 0) ok = wait(&acc_full[2 * half + a], apar);
                     __syncwarp();
                     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -272,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
                 if (col < p.m && tok0 < p.B)
                     sm100::fence_proxy_async_smem(), __syncwarp();
                 if (lane == 0 && col < p.m && tok0 < p.B) {
-                    tma_store_2d(&ymap, out - lane * 128 + slot * CHUNK, col, tok0);
+                    tma_store_2d(&ymap, out - lane * 128 + slot * CHUNK, col, w.ks * p.part_rows + tok0);
                     bulk_commit();
                 }
             };
@@ -316,6 +331,22 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
     }
 }
 
+// y = the parts of a split K, added in order; four columns a thread
+__global__ void __launch_bounds__(256) fp8_sum_parts_kernel(const float *part, int64_t part_stride, int parts, void *y,
+                                                            int y_dtype, int64_t quads) {
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
+        float4 sum = __ldcg(reinterpret_cast<const float4 *>(part) + i);
+#pragma unroll 4
+        for (int k = 1; k < parts; ++k) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + k * part_stride) + i);
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        store_y4(y, y_dtype, i * 4, sum);
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const CUtensorMap &qmap, const CUtensorMap &wmap,
@@ -329,8 +360,36 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const CUtensorMap &qmap, con
     Fp8GemmParams q = p;
     CUtensorMap a = qmap, b = wmap, c = ymap;
     void *args[] = {&a, &b, &c, &q};
-    const int clusters = p.tiles < num_sms / 2 ? p.tiles : num_sms / 2;
+    const int items = p.tiles * p.ksplit, clusters = items < num_sms / 2 ? items : num_sms / 2;
     return launch_ex(fn, dim3(2 * clusters), dim3(THREADS), SMEM, s, pdl, args, 2);
+}
+
+int plan_fp8_gemm(int64_t tiles, int KB, int64_t B, int64_t m, int num_sms) {
+    // A pair of CTAs takes a K block in 0.62 us; an item's start and end cost
+    // about 2 us.  Splitting K over more pairs costs the parts' trip through L2
+    // (8 bytes each at 5 TB/s) and a launch.  (4096 x 14336, 128 tokens: 16
+    // tiles of 112 blocks take 71 us on 16 of 74 pairs, 25 us split in four.)
+    const int pairs = num_sms / 2;
+    int best = 1;
+    double best_t = 1e30;
+    for (int s = 1; s <= 8 && s * 4 <= KB + 3; ++s) {
+        const double waves = (double)((tiles * s + pairs - 1) / pairs);
+        const double t = waves * ((KB + s - 1) / s * 0.62 + 2.0) + (s > 1 ? 3.0 + (double)s * B * m * 8 / 5e6 : 0.0);
+        if (t < best_t * 0.95) {
+            best_t = t;
+            best = s;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_fp8_sum_parts(const float *part, int64_t part_stride, int parts, void *y, int y_dtype, int64_t count,
+                                 cudaStream_t s, bool pdl) {
+    int64_t quads = count / 4;
+    void *args[] = {&part, &part_stride, &parts, &y, &y_dtype, &quads};
+    const int64_t blocks = (quads + 255) / 256;
+    return launch_ex((const void *)fp8_sum_parts_kernel, dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8)), dim3(256), 0,
+                     s, pdl, args);
 }
 
 }  // namespace glq

@@ -145,8 +145,9 @@ struct DeviceGuard {
 };
 
 // The 8-bit float operators' buffers in the device's shared workspace:
-// rounded activations, their scales, all of a mixture-of-experts call.
-enum Fp8Ws { FP8_WS_Q, FP8_WS_S, FP8_WS_MOE, FP8_WS_COUNT };
+// rounded activations, their scales, parts of a split K, all of a mixture-of-
+// experts call.
+enum Fp8Ws { FP8_WS_Q, FP8_WS_S, FP8_WS_Z, FP8_WS_MOE, FP8_WS_COUNT };
 // Makes each at least need[i] bytes (the rules of the shared workspace hold:
 // growth synchronises, and is refused during stream capture).
 glq_status fp8_workspace(int dev, const size_t need[FP8_WS_COUNT], cudaStream_t s, void *out[FP8_WS_COUNT]);
