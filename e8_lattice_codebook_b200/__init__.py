@@ -44,7 +44,7 @@ EXPORTS = (
     "glq_layer_set_batch_invariant", "glq_layer_create_shard", "glq_cast",
     "glq_rht_input_operand", "glq_layer_selftest_wait",
     "glq_fp8_quantize", "glq_fp8_create", "glq_fp8_destroy", "glq_fp8_reserve", "glq_fp8_linear",
-    "glq_fp8_linear_quantized", "glq_fp8_dequant", "glq_fp8_check", "glq_fp8_info",
+    "glq_fp8_linear_quantized", "glq_fp8_dequant", "glq_fp8_check", "glq_fp8_info", "glq_fp8_selftest_wait",
     "glq_moe_create", "glq_moe_destroy", "glq_moe_reserve", "glq_moe_forward", "glq_moe_check", "glq_moe_info",
 )
 
@@ -106,6 +106,7 @@ _SIGNATURES = {
     "glq_fp8_linear_quantized": ([_vp, _vp, _vp, _vp, ctypes.c_int, _i64, _vp], ctypes.c_int),
     "glq_fp8_dequant": ([_vp, _vp, _vp], ctypes.c_int),
     "glq_fp8_check": ([_vp, _vp], ctypes.c_int),
+    "glq_fp8_selftest_wait": ([_vp, ctypes.c_int, _i64, _vp], ctypes.c_int),
     "glq_fp8_info": ([_vp, ctypes.POINTER(_i64), ctypes.POINTER(_i64), ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
     "glq_moe_create": ([ctypes.POINTER(MoeConfig), _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(_vp)], ctypes.c_int),
     "glq_moe_destroy": ([_vp], ctypes.c_int),
@@ -380,6 +381,10 @@ def glq_fp8_dequant(handle, w_ptr, stream) -> None:
 
 def glq_fp8_check(handle, stream) -> None:
     _ok(_L().glq_fp8_check(handle, stream), "glq_fp8_check")
+
+
+def glq_fp8_selftest_wait(handle, arrivals, limit, stream) -> None:
+    _ok(_L().glq_fp8_selftest_wait(handle, arrivals, limit, stream), "glq_fp8_selftest_wait")
 
 
 def glq_fp8_info(handle):
@@ -757,6 +762,11 @@ class Fp8Linear:
         w = torch.empty((self.m, self.n), dtype=torch.float32, device=self.device)
         glq_fp8_dequant(self.handle, w.data_ptr(), _call_stream(self._index, stream, w))
         return w
+
+    def selftest_wait(self, arrivals: int, limit: int, stream=None):
+        """One bounded wait of the kernels on a barrier `arrivals` of its two
+        arrivals reach; the outcome reads back through check()."""
+        glq_fp8_selftest_wait(self.handle, arrivals, limit, _call_stream(self._index, stream))
 
     def check(self, stream=None):
         glq_fp8_check(self.handle, _call_stream(self._index, stream))

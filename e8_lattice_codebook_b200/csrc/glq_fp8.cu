@@ -187,6 +187,9 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
                 const uint8_t *w = p.w + ((int64_t)t * p.KB + k0) * GLQ_FP8_TILE_BYTES;
                 int col = (int)k0 * GLQ_FP8_BLOCK;
                 for (uint32_t k = 0; k < nk; ++k, ++i, w += GLQ_FP8_TILE_BYTES, col += GLQ_FP8_BLOCK, ld.next()) {
+                    // a stage's second use waits for the tokens of its first, and
+                    // a wait must not count the time of the kernel before
+                    if (ROUND && i == (uint32_t)STAGES) pdl_wait();
                     if (ROUND || i >= ahead) {
                         ok = pipe_load<NT, ROUND>(pipe, ld, w, ROUND ? 0 : NT * 128, p.err);
                         if (!ok) break;
@@ -198,6 +201,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
         }
     } else if (warp == 1) {
         if (elect_one()) {
+            pdl_wait();  // (as above)
             pipe_mma<NT>(pipe, smem, 0, nblk, p.err);
             sm100::mma_commit(&pipe.mma_done);  // every MMA issued has completed
             sm100::mbar_wait(&pipe.mma_done, 0, WAIT_CYCLES);
@@ -231,13 +235,13 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
                 for (int r = 0; r < ROWS; ++r) {
                     f.x[r] = make_uint2(0, 0);
                     // n is a multiple of 8: a lane's four columns are in or out together
-                    if (r < p.B && col < p.n) f.x[r] = __ldg(reinterpret_cast<const uint2 *>(src + (int64_t)r * p.n));
+                    if (r < p.B && col < p.n) f.x[r] = __ldcg(reinterpret_cast<const uint2 *>(src + (int64_t)r * p.n));
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < SC; ++j) {
                     const int tok = j * 32 + lane;
-                    f.s[j] = tok < p.B ? p.s[(int64_t)k * p.s_ld + tok] : 0.f;
+                    f.s[j] = tok < p.B ? __ldcg(p.s + (int64_t)k * p.s_ld + tok) : 0.f;
                 }
             }
         };
@@ -404,8 +408,17 @@ cudaError_t prepare(const SkinnyKernel &k) {
 cudaError_t fp8_skinny_clusters(int num_sms, int count[9]) {
     // the clusters that fit depend on the device's layout of SMs and on one
     // CTA per SM, not on which variant runs
+    static int known[128][9];  // per device, once asked
+    static std::atomic<bool> asked[128];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 128 && asked[dev].load(std::memory_order_acquire)) {
+        for (int c = 0; c <= 8; ++c) count[c] = known[dev][c];
+        return cudaSuccess;
+    }
     const SkinnyKernel k = skinny_kernel(2, 16);
-    cudaError_t e = prepare(k);
+    e = prepare(k);
     count[0] = 0;
     count[1] = num_sms;
     for (int c = 2; c <= 8 && e == cudaSuccess; ++c) {
@@ -421,6 +434,10 @@ cudaError_t fp8_skinny_clusters(int num_sms, int count[9]) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         e = cudaOccupancyMaxActiveClusters(&count[c], k.fn, &cfg);
+    }
+    if (e == cudaSuccess && dev < 128) {  // two callers would write the same values
+        for (int c = 0; c <= 8; ++c) known[dev][c] = count[c];
+        asked[dev].store(true, std::memory_order_release);
     }
     return e;
 }

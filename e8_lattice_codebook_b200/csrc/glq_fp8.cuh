@@ -93,9 +93,8 @@ __device__ __forceinline__ uint32_t round4(uint2 w, float inv) {
 }
 
 // ---------------------------------------------------------------------------
-// Waits poll with test_wait, which answers at once.  A try_wait that suspends
-// its thread holds up the waits of the other warps on its scheduler (the
-// drain warps beside the MMA thread saw their barrier 0.5 us after the rest).
+// Waits: CTA scope, bounded.  (try_wait, with and without a suspend hint, took
+// the same time within 5 %, now more, now less.)
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
@@ -109,21 +108,18 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     return done != 0;
 }
 
-// false once the wait has run out, here (then *abort is set and the error
-// word says so) or elsewhere in the CTA
-__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned *err) {
+// false once `limit` cycles have passed, here (then *abort is set and the
+// error word says so) or elsewhere in the CTA
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned *err,
+                                             uint64_t limit = WAIT_CYCLES) {
     if (mbar_test(bar, parity)) return true;
     const uint64_t t0 = sm100::clock_cycles();
     for (;;) {
 #pragma unroll 1
-        for (int i = 0; i < 64; ++i) {
+        for (int i = 0; i < 64; ++i)
             if (mbar_test(bar, parity)) return true;
-#ifdef NAP
-            __nanosleep(NAP);
-#endif
-        }
         if (*abort) return false;
-        if (sm100::clock_cycles() - t0 > WAIT_CYCLES) {
+        if (sm100::clock_cycles() - t0 > limit) {
             atomicOr(err, GLQ_DEVERR_TIMEOUT);
             *abort = 1;
             return false;

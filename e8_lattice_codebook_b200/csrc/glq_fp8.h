@@ -105,6 +105,9 @@ cudaError_t launch_fp8_sum_parts(const float *part, int64_t part_stride, int par
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const CUtensorMap &qmap, const CUtensorMap &wmap,
                             const CUtensorMap &ymap, int num_sms, cudaStream_t s, bool pdl);
 
+// the kernels' bounded wait on a barrier `arrivals` of its two arrivals reach
+cudaError_t launch_fp8_wait_selftest(unsigned *err, int arrivals, unsigned long long limit, cudaStream_t s);
+
 // A mixture-of-experts layer (glq_moe.cu) for T <= MOE_MAX_T tokens.  d: width
 // of x and y, inter: of an expert; KB1 = ceil(d/128) = DB, IB = ceil(inter/128).
 constexpr int MOE_MAX_T = 64, MOE_MAX_E = 512, MOE_MAX_K = 16;

@@ -5,7 +5,9 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
+#include <utility>
 
 #include "../../include/glq.h"
 #include "glq_fp8.h"
@@ -22,15 +24,21 @@ int64_t blocks_of(int64_t v) { return (v + GLQ_FP8_BLOCK - 1) / GLQ_FP8_BLOCK; }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-template <typename T>
-glq_status dev_alloc(T **p, size_t bytes, size_t *total) {
-    *p = nullptr;
-    if (cudaMalloc((void **)p, bytes) != cudaSuccess) {
+// One allocation for several arrays: sizes[i] bytes at *out[i], 256-byte
+// aligned.  *out[0] is what cudaFree takes.
+glq_status dev_alloc(std::initializer_list<std::pair<void **, size_t>> arrays, size_t *total) {
+    size_t bytes = 0;
+    for (const auto &a : arrays) bytes += (a.second + 255) & ~(size_t)255;
+    char *p = nullptr;
+    if (cudaMalloc((void **)&p, bytes) != cudaSuccess) {
         cudaGetLastError();
-        *p = nullptr;
         return GLQ_ERR_OOM;
     }
-    *total += bytes;
+    *total = bytes;
+    for (const auto &a : arrays) {
+        *a.first = p;
+        p += (a.second + 255) & ~(size_t)255;
+    }
     return GLQ_OK;
 }
 
@@ -69,9 +77,7 @@ bool encode_e4m3(CUtensorMap *map, const uint8_t *q, int64_t cols, int64_t rows,
 }
 
 void free_fp8(glq_fp8 L) {
-    cudaFree(L->d_w);
-    cudaFree(L->d_ws);
-    cudaFree(L->d_err);
+    cudaFree(L->d_w);  // and what was allocated with it
     delete L;
 }
 
@@ -190,12 +196,7 @@ glq_status check_word(unsigned *d_err, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 
 void free_moe(glq_moe L) {
-    cudaFree(L->d_w13);
-    cudaFree(L->d_w2);
-    cudaFree(L->d_s13);
-    cudaFree(L->d_s2);
-    cudaFree(L->d_err);
-    cudaFree(L->d_bar);
+    cudaFree(L->d_w13);  // and what was allocated with it
     delete L;
 }
 
@@ -247,6 +248,13 @@ void moe_need(glq_moe L, int64_t T, size_t need[glq::FP8_WS_COUNT]) {
     }
 }
 
+// Layers are not made while their stream is captured: the allocation would end the capture.
+bool capturing(void *stream) {
+    cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &c) != cudaSuccess) cudaGetLastError();
+    return c != cudaStreamCaptureStatusNone;
+}
+
 bool good_dims(int64_t m, int64_t n) {
     return m > 0 && n > 0 && !(m & 7) && !(n & 7) && m <= GLQ_FP8_MAX_DIM && n <= GLQ_FP8_MAX_DIM;
 }
@@ -278,6 +286,7 @@ glq_status glq_fp8_create(int64_t m, int64_t n, const void *w_dev, int64_t ldw, 
     *out = nullptr;
     if (!good_dims(m, n) || ldw < n || (ldw & 7)) return GLQ_ERR_SHAPE;
     if (!w_dev || !scales_dev || !aligned(w_dev, 8) || !aligned(scales_dev, 4)) return GLQ_ERR_INVALID_ARG;
+    if (capturing(stream)) return GLQ_ERR_CAPTURE;
     glq_fp8 L = new (std::nothrow) glq_fp8_s;
     if (!L) return GLQ_ERR_OOM;
     L->m = m;
@@ -292,9 +301,11 @@ glq_status glq_fp8_create(int64_t m, int64_t n, const void *w_dev, int64_t ldw, 
         cudaGetLastError();
         st = GLQ_ERR_CUDA;
     }
-    if (st == GLQ_OK) st = dev_alloc(&L->d_w, (size_t)tiles * GLQ_FP8_TILE_BYTES, &L->device_bytes);
-    if (st == GLQ_OK) st = dev_alloc(&L->d_ws, (size_t)tiles * sizeof(float), &L->device_bytes);
-    if (st == GLQ_OK) st = dev_alloc(&L->d_err, sizeof(unsigned), &L->device_bytes);
+    if (st == GLQ_OK)
+        st = dev_alloc({{(void **)&L->d_w, (size_t)tiles * GLQ_FP8_TILE_BYTES},
+                        {(void **)&L->d_ws, (size_t)tiles * sizeof(float)},
+                        {(void **)&L->d_err, sizeof(unsigned)}},
+                       &L->device_bytes);
     if (st == GLQ_OK) {
         glq::Fp8PackParams p{};
         p.src = static_cast<const uint8_t *>(w_dev);
@@ -392,6 +403,13 @@ glq_status glq_fp8_check(glq_fp8 L, void *stream) {
     return check_word(L->d_err, static_cast<cudaStream_t>(stream));
 }
 
+glq_status glq_fp8_selftest_wait(glq_fp8 L, int arrivals, int64_t limit, void *stream) {
+    if (!L || arrivals < 1 || arrivals > 2 || limit <= 0) return GLQ_ERR_INVALID_ARG;
+    DeviceGuard guard(L->device);
+    return launched(glq::launch_fp8_wait_selftest(L->d_err, arrivals, (unsigned long long)limit,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
 glq_status glq_fp8_info(glq_fp8 L, int64_t *m, int64_t *n, size_t *device_bytes) {
     if (!L) return GLQ_ERR_INVALID_ARG;
     if (m) *m = L->m;
@@ -418,6 +436,7 @@ glq_status glq_moe_create(const glq_moe_config *c, const void *gate_dev, const f
         if (!w || !aligned(w, 8)) return GLQ_ERR_INVALID_ARG;
     for (const float *s : {gate_scales_dev, up_scales_dev, down_scales_dev})
         if (!s || !aligned(s, 4)) return GLQ_ERR_INVALID_ARG;
+    if (capturing(stream)) return GLQ_ERR_CAPTURE;
     glq_moe L = new (std::nothrow) glq_moe_s;
     if (!L) return GLQ_ERR_OOM;
     L->experts = c->experts;
@@ -436,12 +455,14 @@ glq_status glq_moe_create(const glq_moe_config *c, const void *gate_dev, const f
         cudaGetLastError();
         st = GLQ_ERR_CUDA;
     }
-    if (st == GLQ_OK) st = dev_alloc(&L->d_w13, (size_t)tiles13 * GLQ_FP8_TILE_BYTES, &L->device_bytes);
-    if (st == GLQ_OK) st = dev_alloc(&L->d_w2, (size_t)tiles2 * GLQ_FP8_TILE_BYTES, &L->device_bytes);
-    if (st == GLQ_OK) st = dev_alloc(&L->d_s13, (size_t)tiles13 * sizeof(float), &L->device_bytes);
-    if (st == GLQ_OK) st = dev_alloc(&L->d_s2, (size_t)tiles2 * sizeof(float), &L->device_bytes);
-    if (st == GLQ_OK) st = dev_alloc(&L->d_err, sizeof(unsigned), &L->device_bytes);
-    if (st == GLQ_OK) st = dev_alloc(&L->d_bar, sizeof(uint64_t), &L->device_bytes);
+    if (st == GLQ_OK)
+        st = dev_alloc({{(void **)&L->d_w13, (size_t)tiles13 * GLQ_FP8_TILE_BYTES},
+                        {(void **)&L->d_w2, (size_t)tiles2 * GLQ_FP8_TILE_BYTES},
+                        {(void **)&L->d_s13, (size_t)tiles13 * sizeof(float)},
+                        {(void **)&L->d_s2, (size_t)tiles2 * sizeof(float)},
+                        {(void **)&L->d_err, sizeof(unsigned)},
+                        {(void **)&L->d_bar, sizeof(uint64_t)}},
+                       &L->device_bytes);
     if (st == GLQ_OK) {
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         bool ok = cudaMemsetAsync(L->d_err, 0, sizeof(unsigned), s) == cudaSuccess &&

@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
         }
     } else if (warp == 1) {
         if (elect_one()) {
+            pdl_wait();  // a bounded wait must not count the time of the kernel before
             if (rank == 0) {
                 const uint32_t idesc = idesc_e4m3_f32(2 * TOK, COLS);
                 uint32_t s = 0, par = 0, a = 0, apar = 1;
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int kb = min(kb0 + i, w.kb1 - 1);
-                    rs[i] = __ldg(s + (int64_t)kb * p.s_ld);
+                    rs[i] = __ldcg(s + (int64_t)kb * p.s_ld);
                     rw[i] = __ldg(ws + kb);
                 }
             };

@@ -9,6 +9,7 @@
 // that the wait runs out for certain (a flag that nothing sets), with a
 // short limit chosen by the caller; no copy or other memory operation is
 // pending on the barrier.
+#include "glq_fp8.cuh"
 #include "glq_kernels.cuh"
 #include "glq_sm100.cuh"
 
@@ -29,7 +30,26 @@ __global__ void wait_selftest_kernel(unsigned *err, int kind, int arrivals, unsi
     if (!ok) atomicOr(err, GLQ_DEVERR_TIMEOUT);
 }
 
+// The same for the wait of the 8-bit float kernels.
+__global__ void fp8_wait_selftest_kernel(unsigned *err, int arrivals, unsigned long long limit) {
+    __shared__ uint64_t bar;
+    __shared__ volatile int abort;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 2);
+        abort = 0;
+    }
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int i = 0; i < arrivals; ++i) sm100::mbar_arrive(&bar);
+    fp8::wait_bounded(&bar, 0, &abort, err, limit);
+}
+
 }  // namespace
+
+cudaError_t launch_fp8_wait_selftest(unsigned *err, int arrivals, unsigned long long limit, cudaStream_t s) {
+    fp8_wait_selftest_kernel<<<1, 32, 0, s>>>(err, arrivals, limit);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_wait_selftest(unsigned *err, int kind, int arrivals, unsigned long long limit, cudaStream_t s) {
     wait_selftest_kernel<<<1, 32, 0, s>>>(err, kind, arrivals, limit);

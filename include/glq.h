@@ -508,8 +508,8 @@ GLQ_API glq_status glq_fp8_quantize(const void *x_dev, glq_dtype x_dtype, int64_
  *   Both are read on `stream` and copied (re-laid-out for the kernels); they
  *   may be freed once the call returns.  A NaN weight or a non-finite scale
  *   makes the outputs it reaches NaN or infinite.
- * Errors: GLQ_ERR_INVALID_ARG, GLQ_ERR_SHAPE, GLQ_ERR_OOM, GLQ_ERR_CUDA (a
- *   capturing stream among its causes).  Synchronises `stream`.
+ * Errors: GLQ_ERR_INVALID_ARG, GLQ_ERR_SHAPE, GLQ_ERR_OOM, GLQ_ERR_CAPTURE
+ *   (`stream` is being captured), GLQ_ERR_CUDA.  Synchronises `stream`.
  */
 GLQ_API glq_status glq_fp8_create(int64_t m, int64_t n, const void *w_dev, int64_t ldw, const float *scales_dev,
                                   void *stream, glq_fp8 *out);
@@ -525,6 +525,12 @@ GLQ_API glq_status glq_fp8_reserve(glq_fp8 layer, int64_t max_B);
  * glq_fp8_linear -- y = x W^T with x rounded as glq_fp8_quantize does.
  * x_dev: device [B][n] (GLQ_F16 or GLQ_BF16), y_dev: device [B][m] (x's dtype
  * or GLQ_F32), both row-major and 16-byte aligned.  B >= 0 (0 is a no-op).
+ * Paths: up to 64 tokens a kernel bound by reading the weights, whose clusters
+ *   split K (it rounds up to 4 tokens itself; above, a kernel before it does);
+ *   above 64 a tcgen05 GEMM of CTA pairs, which splits K through the shared
+ *   workspace when the output has few tiles.  A batch of more than 8192 runs
+ *   8192 at a time.  A call's results are the same bits run to run; between
+ *   batch sizes a token's may differ in the order of its fp32 sums.
  * Errors as glq_linear.  Asynchronous.
  */
 GLQ_API glq_status glq_fp8_linear(glq_fp8 layer, const void *x_dev, glq_dtype x_dtype, void *y_dev,
@@ -548,6 +554,13 @@ GLQ_API glq_status glq_fp8_dequant(glq_fp8 layer, float *w_dev, void *stream);
 
 /* glq_fp8_check -- glq_layer_check for an 8-bit float layer. */
 GLQ_API glq_status glq_fp8_check(glq_fp8 layer, void *stream);
+
+/*
+ * glq_fp8_selftest_wait -- glq_layer_selftest_wait for the bounded wait of the
+ * 8-bit float kernels (limit in SM clock cycles).  Read the outcome with
+ * glq_fp8_check.  Errors: GLQ_ERR_INVALID_ARG, GLQ_ERR_CUDA.  Asynchronous.
+ */
+GLQ_API glq_status glq_fp8_selftest_wait(glq_fp8 layer, int arrivals, int64_t limit, void *stream);
 
 /* Layer geometry.  Any output may be NULL. */
 GLQ_API glq_status glq_fp8_info(glq_fp8 layer, int64_t *m, int64_t *n, size_t *device_bytes);

@@ -82,6 +82,8 @@ LINEAR = [  # m, n, B: one block, ends inside a block, fewer blocks than SMs, ma
     (8, 8, 1), (128, 128, 16), (136, 264, 5), (960, 960, 1), (2560, 960, 2), (8, 4096, 7), (4096, 1024, 16),
     (264, 1160, 17), (1024, 512, 32), (200, 392, 33), (1032, 648, 64), (392, 520, 65), (640, 2048, 100), (256, 256, 128),
     (520, 136, 129), (384, 1032, 300), (1536, 1024, 512), (776, 776, 1000),
+    # K split over pairs: 2 to 8 parts, ends inside a block, an odd number of row blocks
+    (128, 4096, 66), (392, 3080, 200), (1032, 2056, 257),
 ]
 
 
@@ -241,3 +243,35 @@ def test_refusals(glq):
     with pytest.raises(glq.GlqError) as e:
         glq.fp8_quantize(torch.zeros(2, 12, device="cuda"))
     assert e.value.status == 2
+
+
+def test_wait_runs_out_and_reports(glq):
+    gen = torch.Generator().manual_seed(25)
+    layer, w, s = _layer(glq, gen, 136, 264)
+    layer.selftest_wait(1, 2_000_000)  # an arrival that never comes: about 1 ms
+    with pytest.raises(glq.GlqError) as e:
+        layer.check()
+    assert e.value.status == 9
+    layer.check()  # cleared
+    layer.selftest_wait(2, 2_000_000)
+    layer.check()
+    x = _x(gen, 3, 264, torch.bfloat16)
+    _check(layer(x.cuda()), x, w, s, torch.bfloat16)  # the context is whole
+    for bad in ((0, 10), (3, 10), (1, 0)):
+        with pytest.raises(glq.GlqError) as e:
+            layer.selftest_wait(*bad)
+        assert e.value.status == 1
+
+
+def test_no_layer_while_capturing(glq):
+    gen = torch.Generator().manual_seed(26)
+    w, s = (t.cuda() for t in ref.random_weight(gen, 136, 136))
+    y = torch.zeros(8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(glq.GlqError) as e:
+            glq.Fp8Linear(w, s)
+        y.add_(1)
+    assert e.value.status == 11
+    graph.replay()
+    assert torch.all(y == 1)  # the capture was not disturbed

@@ -55,6 +55,8 @@ def _inputs(gen, T, E, d, dtype):
 SIZES = [  # T, E, k, d, inter: one block; widths that end inside a block; every token tile; all experts; many per lane
     (1, 1, 1, 8, 8), (1, 8, 2, 256, 128), (3, 5, 5, 136, 264), (7, 64, 6, 320, 200), (16, 8, 3, 512, 384), (17, 12, 4, 264, 136),
     (32, 6, 2, 128, 520), (33, 9, 4, 392, 264), (64, 4, 2, 256, 256), (64, 130, 8, 136, 72), (5, 300, 16, 72, 40), (1, 512, 16, 64, 16),
+    # the largest tables in shared memory, for each token tile
+    (64, 512, 16, 16, 8), (32, 512, 16, 8, 16), (16, 512, 16, 16, 16), (4, 9, 9, 264, 136),
 ]
 
 
