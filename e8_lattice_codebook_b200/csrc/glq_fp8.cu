@@ -3,6 +3,8 @@
 //     y[b][r] = sum_kb s[kb][b] ws[r/128][kb] sum_{k in kb} q[b][k] w[r][k]
 // (q, w e4m3; s the token's scale of 128-column block kb, ws the weight
 // block's).
+#include <type_traits>
+
 #include "glq_fp8.cuh"
 #include "glq_kernels.cuh"
 
@@ -13,32 +15,81 @@ namespace {
 using namespace fp8;
 
 // ---------------------------------------------------------------------------
-// Quantiser: reads x once, writes q and s once; bound by HBM.  A CTA takes 32
-// tokens x 2 groups: half a warp per group (8 values a lane, one or two
-// 16-byte loads), all of a warp's four tokens loaded before the first is
-// used, and the scales of a group of 32 tokens leave as one 128-byte line of
-// the [group][token] array.
+// Quantiser: reads x once, writes q and s once; bound by HBM, so instructions
+// are kept few.  A CTA takes 32 tokens x 2 groups: half a warp per group (8
+// values a lane, one or two 16-byte loads), all of a warp's four tokens loaded
+// before the first is used.  16-bit magnitudes are compared as they are, two
+// tokens to a register; the divisions are made once per token and group, by
+// the lane whose turn the token is.  The scales of 32 tokens leave as one
+// 128-byte line of the [group][token] array.
 // ---------------------------------------------------------------------------
 
 constexpr int QT = 32, QG = 2, QTHREADS = 256;
+constexpr int QPER = QT / (QTHREADS / 32);  // tokens per warp
+static_assert(QPER == 4, "a pair of tokens in each of two registers");
 
+// Eight values of a lane, as loaded.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float v[8]) {
-    const uint4 w = ldg_nc_v4(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<T>(u[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+struct Eight {
+    uint4 w;
+    __device__ __forceinline__ void load(const T *p) { w = ldg_nc_v4(p); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    // the largest magnitude in each half, as 16-bit patterns
+    __device__ __forceinline__ uint32_t top() const {
+        constexpr uint32_t M = 0x7FFF7FFFu;
+        return __vmaxu2(__vmaxu2(w.x & M, w.y & M), __vmaxu2(w.z & M, w.w & M));
     }
+    __device__ __forceinline__ uint2 round(float inv) const {
+        const float2 a = unpack2<T>(w.x), b = unpack2<T>(w.y), c = unpack2<T>(w.z), d = unpack2<T>(w.w);
+        const float v[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+        return make_uint2(e4m3x4(v, inv), e4m3x4(v + 4, inv));
+    }
+};
+template <>
+struct Eight<float> {
+    float v[8];
+    __device__ __forceinline__ void load(const float *p) {
+        const uint4 a = ldg_nc_v4(p), b = ldg_nc_v4(p + 4);
+        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+    __device__ __forceinline__ uint2 round(float inv) const { return make_uint2(e4m3x4(v, inv), e4m3x4(v + 4, inv)); }
+};
+
+// The bits of the group's largest magnitude (fp32) of token l16 & 3, over the
+// 16 lanes of half a warp.
+template <typename T>
+__device__ __forceinline__ uint32_t half_warp_top(const Eight<T> (&e)[QPER], int l16) {
+    uint32_t m[2];  // tokens 0 and 1, 2 and 3
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t a = e[2 * i].top(), b = e[2 * i + 1].top();
+        m[i] = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m[i] = __vmaxu2(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+    }
+    const uint32_t p = (l16 & 2) ? m[1] : m[0], bits = (l16 & 1) ? p >> 16 : p & 0xFFFFu;
+    if constexpr (std::is_same<T, __half>::value) return __float_as_uint(__half2float(__ushort_as_half((unsigned short)bits)));
+    else return bits << 16;
 }
 template <>
-__device__ __forceinline__ void load8<float>(const float *p, float v[8]) {
-    const uint4 a = ldg_nc_v4(p), b = ldg_nc_v4(p + 4);
-    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ uint32_t half_warp_top<float>(const Eight<float> (&e)[QPER], int l16) {
+    uint32_t mine = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+    for (int i = 0; i < QPER; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, mag_bits(e[i].v[j]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if ((l16 & 3) == i) mine = m;
+    }
+    return mine;
 }
 
 template <typename T>
@@ -50,31 +101,21 @@ __global__ void __launch_bounds__(QTHREADS) fp8_quantize_kernel(Fp8QuantParams p
     const int64_t t0 = (int64_t)blockIdx.y * QT;
     const int g = blockIdx.x * QG + half;
     const int col = g * GLQ_FP8_BLOCK + l16 * 8;
-    constexpr int PER = QT / (QTHREADS / 32);  // tokens per warp
-    float v[PER][8];
+    Eight<T> e[QPER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int64_t t = t0 + warp + i * (QTHREADS / 32);
-        if (t < p.B && col < p.n) load8(static_cast<const T *>(p.x) + t * p.n + col, v[i]);
-        else
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    for (int i = 0; i < QPER; ++i) {
+        const int64_t t = t0 + warp * QPER + i;
+        if (t < p.B && col < p.n) e[i].load(static_cast<const T *>(p.x) + t * p.n + col);
+        else e[i].zero();
     }
+    const uint32_t top = max(half_warp_top<T>(e, l16), FLOOR_BITS);
+    const float inv = group_inv(top);
+    if (l16 < QPER) s_s[half][warp * QPER + l16] = group_scale(top);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int tl = warp + i * (QTHREADS / 32);
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, mag_bits(v[i][j]));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        m = max(m, FLOOR_BITS);
-        const float inv = group_inv(m);
-        if (t0 + tl < p.B && g < p.KB) {
-            const uint2 q = make_uint2(e4m3x4(v[i], inv), e4m3x4(v[i] + 4, inv));
-            *reinterpret_cast<uint2 *>(p.q + (t0 + tl) * ((int64_t)p.KB * GLQ_FP8_BLOCK) + col) = q;
-        }
-        if (l16 == 0) s_s[half][tl] = group_scale(m);
+    for (int i = 0; i < QPER; ++i) {
+        const int64_t t = t0 + warp * QPER + i;
+        const uint2 q = e[i].round(__shfl_sync(0xffffffffu, inv, (lane & 16) + i));
+        if (t < p.B && g < p.KB) *reinterpret_cast<uint2 *>(p.q + t * ((int64_t)p.KB * GLQ_FP8_BLOCK) + col) = q;
     }
     __syncthreads();
     if (threadIdx.x < QG * QT) {
