@@ -3,6 +3,7 @@
 //     y[b][r] = sum_kb s[kb][b] ws[r/128][kb] sum_{k in kb} q[b][k] w[r][k]
 // (q, w e4m3; s the token's scale of 128-column block kb, ws the weight
 // block's).
+#include <cmath>
 #include <type_traits>
 
 #include "glq_fp8.cuh"
@@ -167,7 +168,8 @@ __global__ void __launch_bounds__(256) fp8_dequant_kernel(const uint8_t *tiles, 
 // output tile is 128 weight rows x all tokens; a cluster of C CTAs (one per SM)
 // takes tile after tile, each CTA 1 / C of its K blocks, so that few tiles
 // still keep most SMs loading.  The parts meet in distributed shared memory:
-// token j is summed by CTA j mod C of the cluster, in the order of the CTAs.
+// group j of four tokens is summed by CTA j mod C of the cluster, in the order
+// of the CTAs.
 // (Parts through global memory, summed by the CTA that arrives last, cost 3.5
 // to 5 us at the end of every call: store, atomic and load each make the trip
 // to L2.)
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
         const int quadrant = warp & 3, set = (warp - D_WARP0) >> 2;
         const int row_l = 32 * quadrant + lane, dtid = tid - D_WARP0 * 32;
         float *red = reinterpret_cast<float *>(smem + STAGES * Pipe<NT>::STAGE_BYTES);
-        const int per = (NT + C - 1) / C;  // most tokens one CTA sums
+        const int per = (NT / 4 + C - 1) / C;  // most groups of four tokens one CTA sums
         float acc[HALF];
         uint32_t i = 0, round = 0;
         for (uint32_t t = first; t < tiles; t += NC, ++round) {
@@ -345,29 +347,46 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
                 }
                 continue;
             }
-            // parts to the CTAs that sum them
-            const int mine = live > (int)rank ? (live - (int)rank - 1) / (int)C + 1 : 0;  // tokens this CTA sums
+            // Parts to the CTAs that sum them, four tokens a store (stores of one
+            // token each cost 2.5 us more at 64 tokens), but a single token by
+            // itself (0.1 to 0.5 us less than with three that are not there).
+            const int width = live == 1 ? 1 : 4;
+            const int groups = (live + 3) >> 2;
+            const int mine = groups > (int)rank ? (groups - (int)rank - 1) / (int)C + 1 : 0;  // this CTA sums
             if (!met) cluster_wait(), met = true;
             if (!pipe.wait_warp(&pipe.red_empty, (round & 1) ^ 1, p.err)) break;
-            if (dtid == 0) mbar_expect_tx(&pipe.red_full, (uint32_t)(mine * (int)C) * 512);
+            if (dtid == 0) mbar_expect_tx(&pipe.red_full, (uint32_t)(mine * (int)C * width) * (128 * 4));
+            if (width == 1) {
+                if (set == 0)
+                    st_async(remote_smem(red + (int)rank * 128 + row_l, 0), acc[0], remote_smem(&pipe.red_full, 0));
+            } else {
 #pragma unroll
-            for (int j = 0; j < HALF; ++j) {
-                const int tok = set * HALF + j, own = tok / C, to = tok - own * C;
-                if (tok < live)
-                    st_async(remote_smem(red + ((int)rank * per + own) * 128 + row_l, to), acc[j],
-                             remote_smem(&pipe.red_full, to));
+                for (int j = 0; j < HALF; j += 4) {
+                    const int g = (set * HALF + j) >> 2, own = g / (int)C, to = g - own * (int)C;
+                    if (g < groups)
+                        st_async4(remote_smem(red + (((int)rank * per + own) * 128 + row_l) * 4, to), acc + j,
+                                  remote_smem(&pipe.red_full, to));
+                }
             }
             if (!pipe.wait_warp(&pipe.red_full, round & 1, p.err)) break;
-            // a warp sums one token in eight, a lane four rows
-            const int row = t * 128 + lane * 4;
-            for (int own = dtid >> 5; own < mine; own += D_WARPS) {
-                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (uint32_t c = 0; c < C; ++c) {
-                    const float4 v = *reinterpret_cast<const float4 *>(red + ((int)c * per + own) * 128 + lane * 4);
-                    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            // a warp sums 32 rows of a group
+            for (int u = dtid >> 5; u < mine * 4; u += D_WARPS) {
+                const int own = u >> 2, r = (u & 3) * 32 + lane, row = t * 128 + r;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                if (width == 1) {
+                    for (uint32_t c = 0; c < C; ++c) sum[0] += red[c * 128 + r];
+                } else {
+                    for (uint32_t c = 0; c < C; ++c) {
+                        const float4 v = *reinterpret_cast<const float4 *>(red + (((int)c * per + own) * 128 + r) * 4);
+                        sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
+                    }
                 }
-                // m is a multiple of 8: four rows are in or out together
-                if (row < p.m) store_y4(p.y, p.y_dtype, (int64_t)(own * (int)C + (int)rank) * p.m + row, sum);
+                const int tok = (own * (int)C + (int)rank) * 4;
+                if (row < p.m) {
+#pragma unroll
+                    for (int l = 0; l < 4; ++l)
+                        if (tok + l < live) store_y(p.y, p.y_dtype, (int64_t)(tok + l) * p.m + row, sum[l]);
+                }
             }
             __syncwarp();
             // in the last round nobody waits for it, and a CTA may leave as soon
@@ -483,19 +502,27 @@ cudaError_t fp8_skinny_clusters(int num_sms, int count[9]) {
     return e;
 }
 
-Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, const int clusters[9]) {
-    // One CTA takes a block in about 0.22 us by itself, all together at the
-    // HBM's rate (16 KB at 5.9 TB/s: 0.0028 us); summing the parts of a split
-    // tile costs about as much as four blocks.
+Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, int nt, const int clusters[9]) {
+    // A call takes about 2.4 us beside its blocks.  One CTA takes a block in
+    // 0.22 us (16 tokens) to 0.4 us (64) by itself, all together at the HBM's
+    // rate (16 KB at 5.9 TB/s: 0.0028 us), and near both bounds the two add up
+    // like a norm.  Summing the parts of a split tile costs 1 us at 16 tokens,
+    // 2.5 us at 64, and more the larger the cluster.  Measured with C = 1, 2,
+    // 3, 4, 6, 8 at one token: 4096x14336 28.8, 17.0, 13.9, 12.6, 15.2, 17.2 us
+    // (plan 4); 5120x32768 61, 35, 27.7, 38, 30, 33 us (plan 3); 11008x2048 7.0,
+    // 8.3, 10.5, 9.6, 13.1, 16.0 us (plan 1); 1024x8192 17.3, 11.2, 8.8, 7.3, 6.2,
+    // 5.4 us (plan 8).  At 64 tokens: 2560x960 6.6, 7.9, 7.5, 6.8, 7.7, 11.0 us
+    // (plan 1); 4096x4096 16.1, 13.1, 11.8, 10.7, 14.2, 17.3 us (plan 4).
     Fp8SkinnyPlan best{1, (int)(tiles < clusters[1] ? tiles : clusters[1])};
     double best_t = 1e30;
     for (int c = 1; c <= 8 && c <= KB; ++c) {
         if (clusters[c] < 1) continue;
         const int64_t nc = tiles < clusters[c] ? tiles : clusters[c];
         const int64_t rounds = (tiles + nc - 1) / nc;
-        const double alone = rounds * ((KB + c - 1) / c) * 0.22;
+        const double alone = (double)(rounds * ((KB + c - 1) / c)) * (0.16 + 0.00375 * nt);
         const double hbm = (double)tiles * KB * 0.0028;
-        const double t = (alone > hbm ? alone : hbm) + (c > 1 ? 0.9 : 0.0);
+        const double t = 2.4 + std::cbrt(alone * alone * alone + hbm * hbm * hbm) +
+                         (c > 1 ? 0.4 + nt / 32.0 + 0.1 * c : 0.0);
         if (t < best_t * 0.98) {
             best_t = t;
             best = {c, (int)nc};

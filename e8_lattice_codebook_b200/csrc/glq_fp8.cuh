@@ -223,8 +223,9 @@ struct Pipe {
     // barrier tells phases apart only one back, so X_TURN may not exceed the
     // stages.
     static constexpr int X_TURN = STAGES < X_WARPS ? STAGES : X_WARPS;
-    // parts of the tokens a CTA sums: at most NT / C + 1 tokens from each of C <= 8 CTAs
-    static constexpr int RED_BYTES = (NT + 8) * 128 * 4;
+    // parts of the tokens a CTA sums, in groups of four tokens (2 KB): from each
+    // of C <= 8 CTAs ceil(NT / 4 / C) groups, all of them fewer than NT / 4 + C
+    static constexpr int RED_BYTES = (NT / 4 + 7) * 128 * 16;
     static constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + RED_BYTES;
     static_assert(SMEM_BYTES + 4096 <= 227 * 1024, "shared memory");
 
@@ -401,12 +402,19 @@ __device__ __forceinline__ uint32_t remote_smem(const void *local, uint32_t rank
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(local)), "r"(rank));
     return r;
 }
-// Store into another CTA's shared memory that counts its 4 bytes on a barrier
+// Stores into another CTA's shared memory that count their bytes on a barrier
 // there: the reader waits for the data itself, no store has to be
 // acknowledged before an arrival may follow it.
 __device__ __forceinline__ void st_async(uint32_t addr, float v, uint32_t bar) {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
                  "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async4(uint32_t addr, const float *v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(
+                     addr),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+                 "r"(__float_as_uint(v[3])), "r"(bar)
                  : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }

@@ -75,7 +75,7 @@ cudaError_t fp8_skinny_clusters(int num_sms, int count[9]);
 struct Fp8SkinnyPlan {
     int C, clusters;
 };
-Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, const int clusters[9]);
+Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, int nt, const int clusters[9]);
 // qmap: source 2 only, boxes of 128 columns x nt tokens of q, 128-byte swizzle
 cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, const CUtensorMap &qmap, int source, int nt, int clusters,
                               cudaStream_t s, bool pdl);

@@ -172,7 +172,7 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
     p.RT = L->RT;
     p.KB = L->KB;
     p.err = L->d_err;
-    const glq::Fp8SkinnyPlan plan = glq::plan_fp8_skinny(p.RT, p.KB, L->clusters);
+    const glq::Fp8SkinnyPlan plan = glq::plan_fp8_skinny(p.RT, p.KB, nt, L->clusters);
     p.C = plan.C;
     CUtensorMap qmap{};
     if (source == 2 && !encode_e4m3(&qmap, q, (int64_t)L->KB * GLQ_FP8_BLOCK, B, nt)) return GLQ_ERR_CUDA;
