@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
             bool ok = true;
             for (uint32_t k = 0; k < nk && ok;) {
                 const int n = min((int)(nk - k), DRAIN);
-                if (n == DRAIN) ok = pipe_drain<NT, DRAIN, false>(pipe, i, quadrant, set, acc, p.err);
-                else ok = pipe_drain<NT, 1, false>(pipe, i, quadrant, set, acc, p.err);
+                if (n == DRAIN) ok = pipe_drain<NT, DRAIN>(pipe, i, quadrant, set, acc, p.err);
+                else ok = pipe_drain<NT, 1>(pipe, i, quadrant, set, acc, p.err);
                 k += n == DRAIN ? DRAIN : 1;
                 i += n == DRAIN ? DRAIN : 1;
             }

@@ -349,9 +349,7 @@ __device__ __forceinline__ void pipe_x_done(Pipe<NT> &p, uint32_t it, int lane) 
 // A drain warp: adds blocks it .. it + N - 1 to acc (its half of the tokens).
 // The last block's wait covers the others (MMAs complete in order); several
 // blocks share its cost, about 300 cycles for wait, TMEM load and arrive.
-// SKIP_ZERO: tokens whose scale is 0 take no part (their operand rows are not
-// written).
-template <int NT, int N, bool SKIP_ZERO>
+template <int NT, int N>
 __device__ __forceinline__ bool pipe_drain(Pipe<NT> &p, uint32_t it, int quadrant, int set, float (&acc)[NT / 2],
                                            unsigned *err) {
     constexpr int HALF = NT / 2, STAGES = Pipe<NT>::STAGES;
@@ -381,9 +379,7 @@ __device__ __forceinline__ bool pipe_drain(Pipe<NT> &p, uint32_t it, int quadran
                 const float4 f = sc[j >> 2];
                 const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                for (int l = 0; l < 4; ++l)
-                    if (!SKIP_ZERO || fs[l] != 0.f)
-                        acc[c + j + l] = fmaf(__uint_as_float(d[n][j + l]), fs[l], acc[c + j + l]);
+                for (int l = 0; l < 4; ++l) acc[c + j + l] = fmaf(__uint_as_float(d[n][j + l]), fs[l], acc[c + j + l]);
             }
         }
     }

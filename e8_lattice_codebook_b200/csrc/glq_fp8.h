@@ -125,14 +125,16 @@ struct MoeParams {
     const float *s13;    // [E][2 IB][KB1]
     const uint8_t *w2;   // tiles [E][DB][IB]
     const float *s2;     // [E][DB][IB]
-    // workspace (nt: moe_tile(T), A: experts in use)
-    uint8_t *xq;         // [KB1] operand tiles of nt x 128
-    float *xs;           // [KB1][nt]
-    float *main;         // [T k][2 IB][128]
-    float *spill;        // [grid][nt][128]
-    uint8_t *hq;         // [A][IB] operand tiles of nt x 128
-    float *hs;           // [A][IB][nt]
-    float *part;         // [grid][2][nt][128]
+    // workspace (nt: moe_tile(T), the most a token tile may hold; rows: the tokens of each expert in use,
+    // rounded up to 8, one expert after the other)
+    uint8_t *xq;         // [expert in use][KB1][its rows][128]: x^ as operand tiles
+    float *xs;           // [KB1][T]
+    float *main1;        // [T k][2 IB][128]
+    float *spill1;       // [grid][nt][128]
+    uint8_t *hq;         // [expert in use][IB][its rows][128]: h^ as operand tiles
+    float *hs;           // [expert in use][IB][its rows]
+    float *main2;        // [T k][DB][128]
+    float *spill2;       // [grid][nt][128]
     uint64_t *bar;       // grid barrier: arrivals so far, a multiple of grid between calls
     unsigned *err;
 };

@@ -205,19 +205,21 @@ void free_moe(glq_moe L) {
 size_t moe_workspace(glq_moe L, glq::MoeParams &p, uint8_t *base) {
     const size_t nt = glq::moe_tile(p.T), slots = (size_t)p.T * p.k;
     const size_t A = std::min<size_t>((size_t)L->experts, slots);
+    const size_t rows = slots + 7 * A;  // every expert's tokens rounded up to 8, at most
     size_t off = 0;
     auto take = [&](size_t bytes) {
         uint8_t *r = base ? base + off : nullptr;
         off += (bytes + 255) & ~(size_t)255;
         return r;
     };
-    p.xq = take((size_t)p.KB1 * nt * 128);
-    p.xs = reinterpret_cast<float *>(take((size_t)p.KB1 * nt * 4));
-    p.main = reinterpret_cast<float *>(take(slots * 2 * p.IB * 512));
-    p.spill = reinterpret_cast<float *>(take((size_t)L->num_sms * nt * 512));
-    p.hq = take(A * p.IB * nt * 128);
-    p.hs = reinterpret_cast<float *>(take(A * p.IB * nt * 4));
-    p.part = reinterpret_cast<float *>(take((size_t)L->num_sms * 2 * nt * 512));
+    p.xq = take(rows * p.KB1 * 128);
+    p.xs = reinterpret_cast<float *>(take((size_t)p.KB1 * p.T * 4));
+    p.main1 = reinterpret_cast<float *>(take(slots * 2 * p.IB * 512));
+    p.spill1 = reinterpret_cast<float *>(take((size_t)L->num_sms * nt * 512));
+    p.hq = take(rows * p.IB * 128);
+    p.hs = reinterpret_cast<float *>(take(rows * p.IB * 4));
+    p.main2 = reinterpret_cast<float *>(take(slots * p.DB * 512));
+    p.spill2 = reinterpret_cast<float *>(take((size_t)L->num_sms * nt * 512));
     return off;
 }
 

@@ -9,18 +9,19 @@
 //
 // Bound by HBM: the weights of every chosen expert are read once, 16 KB tile
 // by tile (glq_fp8.h), by the few-token pipeline of glq_fp8.cuh, whose MMA
-// takes all tokens as its N side whichever expert the tile belongs to (the
-// tensor cores have time to spare; a token that did not choose the expert is
-// dropped when the result is read).  The tiles of a phase form one sequence,
-// dealt out evenly over the CTAs, one per SM, so that an odd number of experts
-// or rows leaves no SM idle; a tile that falls to two or more CTAs is summed
-// by whoever reads it, in the order of the CTAs.  Phases, with a barrier over
-// the grid (a cooperative launch) after each:
+// takes the expert's own tokens as its N side, one behind the other: with all
+// tokens there a stage has to hold 64 of them, and 7 stages instead of 11 kept
+// too few weights in flight (64 tokens of 32 experts of 4096 x 2048: 177 us
+// instead of 148).  The tiles of a phase form
+// one sequence, expert by expert, dealt out evenly over the CTAs, one per SM,
+// so that an odd number of experts or rows leaves no SM idle; a tile that falls
+// to two or more CTAs is summed by whoever reads it, in the order of the CTAs.
+// Phases, with a barrier over the grid (a cooperative launch) after each:
 //   0  every CTA: the routing of all tokens, for itself; a share of x^
 //   1  gate and up tiles -> fp32 sums per (token, expert)
 //   h  silu, product, rounding -> h^ as operand tiles
-//   2  down tiles -> sums per token over experts; whole tiles go to y
-//   y  the tiles of y that were split
+//   2  down tiles -> fp32 sums per (token, expert)
+//   y  their sum over the token's experts, in the order of its choices
 // The copy warp runs ahead across the barriers: while a CTA waits, its first
 // stages of the next phase's weights (up to 11 x 16 KB) are on their way.
 #include "glq_fp8.cuh"
@@ -36,25 +37,27 @@ constexpr int WARPS = D_WARP0 + D_WARPS + 1;  // the pipeline's and one that kee
 constexpr int THREADS = WARPS * 32;           // 608
 constexpr int GRID_WARP = WARPS - 1;
 constexpr int H_WARPS = X_WARPS + D_WARPS;    // warps that form h^
-constexpr uint8_t NONE = 0xFF;
 constexpr int LOCAL_T = 4;
 
 // Shared memory behind the stages.
 struct Layout {
-    uint32_t mask, wts, rank, list, ids, slot, end;
+    uint32_t mask, wts, rank, ids, list, off, roff, pairs, end;
 };
-__host__ __device__ inline Layout layout_of(uint32_t base, int nt, int T, int E, int k) {
+__host__ __device__ inline Layout layout_of(uint32_t base, int T, int E, int k) {
     const int most = E < T * k ? E : T * k;  // experts in use, at most
     Layout l;
     l.mask = base;                                  // [E] 64-bit: tokens that chose the expert
     l.wts = l.mask + (uint32_t)E * 8;               // [T][k] fp32: p
     l.rank = l.wts + (uint32_t)(T * k) * 4;         // [E] 16-bit: place among the experts in use
-    l.list = l.rank + (uint32_t)E * 2;              // [most] 16-bit: experts in use
-    l.ids = l.list + (uint32_t)most * 2;            // [T][k] 16-bit: chosen experts, -1 none
-    l.slot = (l.ids + (uint32_t)(T * k) * 2 + 15) & ~15u;  // [most][nt]: which of t's choices, or NONE
-    l.end = l.slot + (uint32_t)most * nt;
+    l.ids = l.rank + (uint32_t)E * 2;               // [T][k] 16-bit: chosen experts, -1 none
+    l.list = l.ids + (uint32_t)(T * k) * 2;         // [most] 16-bit: experts in use
+    l.off = l.list + (uint32_t)most * 2;            // [most + 1] 16-bit: their tokens' first place in pairs
+    l.roff = l.off + (uint32_t)(most + 1) * 2;      // [most + 1] 16-bit: the same with each rounded up to 8
+    l.pairs = l.roff + (uint32_t)(most + 1) * 2;    // [T k] 16-bit: 16 t + which of t's choices, by expert
+    l.end = l.pairs + (uint32_t)(T * k) * 2;
     return l;
 }
+static_assert(MOE_MAX_K <= 16 && MOE_MAX_T <= 64 && 8 * MOE_MAX_T * MOE_MAX_K < 65536, "16-bit tables");
 
 // Monotonic key of a logit: larger for larger values, 0 for those never chosen
 // (NaN, -inf); -0 counts as 0.
@@ -139,112 +142,59 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(
 
 __device__ __forceinline__ float silu(float v) { return v / (1.f + expf(-v)); }
 
-// A scale warp, block i: the group w of T tokens rounded into the operand tile.
+// A scale warp, block i: the group w of `live` tokens rounded into the operand tile.
 template <int NT, typename T16>
-__device__ __forceinline__ bool put_rounded(Pipe<NT> &pipe, uint8_t *smem, uint32_t i, const uint2 (&w)[LOCAL_T], int T,
-                                            float ws, int lane, unsigned *err) {
+__device__ __forceinline__ bool put_rounded(Pipe<NT> &pipe, uint8_t *smem, uint32_t i, const uint2 (&w)[LOCAL_T],
+                                            int live, float ws, int lane, unsigned *err) {
     float inv;
-    const float s = warp_group_scales<T16, LOCAL_T>(w, T, lane, inv);
+    const float s = warp_group_scales<T16, LOCAL_T>(w, live, lane, inv);
     if (!pipe_x_begin(pipe, i, err)) return false;
     uint8_t *xt = pipe_x_tile<NT>(smem, i);
-    if (lane < NT) pipe.sc[i % Pipe<NT>::STAGES][lane] = lane < T ? s * ws : 0.f;
+    if (lane < NT) pipe.sc[i % Pipe<NT>::STAGES][lane] = lane < live ? s * ws : 0.f;
 #pragma unroll
-    for (int t = 0; t < LOCAL_T; ++t) {
-        if (t >= T) break;
-        *reinterpret_cast<uint32_t *>(xt + sw128(t, lane >> 2) + (lane & 3) * 4) =
-            round4<T16>(w[t], __shfl_sync(0xffffffffu, inv, t));
+    for (int j = 0; j < LOCAL_T; ++j) {
+        if (j >= live) break;
+        *reinterpret_cast<uint32_t *>(xt + sw128(j, lane >> 2) + (lane & 3) * 4) =
+            round4<T16>(w[j], __shfl_sync(0xffffffffu, inv, j));
     }
     pipe_x_done<NT, true>(pipe, i, lane);
     return true;
 }
 
-// LOCAL (at most LOCAL_T tokens): x^ and h^ are not shared through memory;
-// every CTA rounds the tokens' columns that its own blocks need into its
-// operand tiles.  The work is done several times over, but two of the four
-// barriers, 2 to 4 us each while the weights saturate the memory, and h's trip
-// through memory go.
-template <int NT, bool LOCAL>
-__global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
+// What every CTA keeps for itself about the routing, and the barriers that do
+// not depend on NT.
+struct Routing {
+    unsigned long long *mask;
+    float *wts;
+    int16_t *rank, *list, *ids;
+    uint16_t *off, *roff, *pairs;
+    uint32_t A;  // experts in use
+    // token t's place among the tokens of expert e
+    __device__ __forceinline__ int place(int e, int t) const { return __popcll(mask[e] & ((1ull << t) - 1)); }
+};
+struct Barriers {
+    // grid[n]: the grid's barrier n has been passed.  part0, part1, formed,
+    // part2: this CTA's warps have written their share of the phase.
+    uint64_t grid[4], part0, part1, formed, part2;
+};
+
+// Everything behind the routing.
+template <int NT, int MAX_NT, bool LOCAL>
+__device__ __forceinline__ void moe_body(const MoeParams &p, const Routing &z, Barriers &bars, Pipe<NT> &pipe,
+                                         uint8_t *smem, uint32_t tmem) {
     using P = Pipe<NT>;
     constexpr int HALF = NT / 2, STAGES = P::STAGES, DRAIN = P::DRAIN;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(16) P pipe;
-    // grid[n]: the grid's barrier n has been passed.  part1, formed, part2:
-    // this CTA's warps have written their share of the phase.
-    __shared__ uint64_t grid_bar[4], part1, formed, part2;
-    __shared__ int s_count;
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x, G = gridDim.x;
-    const int T = p.T, E = p.E, K = p.k;
-    const Layout at = layout_of(STAGES * P::STAGE_BYTES, NT, T, E, K);
-    unsigned long long *mask = reinterpret_cast<unsigned long long *>(smem + at.mask);
-    float *wts = reinterpret_cast<float *>(smem + at.wts);
-    int16_t *rank = reinterpret_cast<int16_t *>(smem + at.rank), *list = reinterpret_cast<int16_t *>(smem + at.list);
-    int16_t *ids = reinterpret_cast<int16_t *>(smem + at.ids);
-    uint8_t *slot = smem + at.slot;
+    const int T = p.T, K = p.k;
+    if constexpr (MAX_NT > 16) {  // (else it has been done)
+        if (warp == 0) pipe.init(lane, 1);
+        if (tid == 0) pipe.tmem = tmem;
+        __syncthreads();
+    }
 
-    // ---------------- phase 0: setup, x^, routing ----------------
-    if (warp == 0) {
-        pipe.init(lane, 1);
-        if (lane == 0) {
-            for (int i = 0; i < 4; ++i) mbar_init(&grid_bar[i], 1);
-            mbar_init(&part1, D_WARPS);
-            mbar_init(&formed, H_WARPS);
-            mbar_init(&part2, D_WARPS);
-        }
-    }
-    if (warp == 1) {
-        sm100::tmem_alloc(&pipe.tmem, P::TMEM_COLS);
-        sm100::tmem_relinquish();
-    }
-    for (int e = tid; e < E; e += THREADS) mask[e] = 0;
-    for (int i = tid; i < (int)(at.end - at.slot) / 4; i += THREADS) reinterpret_cast<uint32_t *>(slot)[i] = 0xFFFFFFFFu;
-    if (tid == 0) prefetch_l2(p.bar);  // before the weights are in flight
-    // this CTA's share of x^: a warp per token and group
-    if constexpr (!LOCAL)
-    for (int i = warp * G + cta; i < T * p.KB1; i += WARPS * G) {
-        const int t = i / p.KB1, kb = i - t * p.KB1, col = kb * GLQ_FP8_BLOCK + lane * 4;
-        uint2 w = make_uint2(0, 0);  // d is a multiple of 8: a lane's four columns are in or out together
-        if (col < p.d) w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.d + col));
-        const float2 a = p.x_dtype ? unpack2<__nv_bfloat16>(w.x) : unpack2<__half>(w.x);
-        const float2 b = p.x_dtype ? unpack2<__nv_bfloat16>(w.y) : unpack2<__half>(w.y);
-        const float v[4] = {a.x, a.y, b.x, b.y};
-        float s;
-        const uint32_t q = warp_quantize(v, s);
-        __stcg(reinterpret_cast<uint32_t *>(p.xq + (int64_t)kb * (NT * 128) + sw128(t, lane >> 2)) + (lane & 3), q);
-        if (lane == 0) __stcg(p.xs + kb * NT + t, s);
-    }
-    if (!LOCAL) fence_proxy_async();  // x^ is read by bulk copies
-    __syncthreads();
-    for (int t = warp; t < T; t += WARPS) {
-        if (E <= 128) route<4>(p, t, lane, ids + t * K, wts + t * K, mask);
-        else route<16>(p, t, lane, ids + t * K, wts + t * K, mask);
-    }
-    sm100::tc_fence_before();
-    __syncthreads();
-    sm100::tc_fence_after();
-    if (warp == 0) {  // experts in use, in order
-        int n = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const bool used = e0 + lane < E && mask[e0 + lane] != 0;
-            const unsigned b = __ballot_sync(0xffffffffu, used);
-            if (used) {
-                const int r = n + __popc(b & ((1u << lane) - 1));
-                rank[e0 + lane] = (int16_t)r;
-                list[r] = (int16_t)(e0 + lane);
-            }
-            n += __popc(b);
-        }
-        if (lane == 0) s_count = n;
-    }
-    __syncthreads();
-    for (int i = tid; i < T * K; i += THREADS)
-        if (ids[i] >= 0) slot[rank[ids[i]] * NT + i / K] = (uint8_t)(i % K);
-    __syncthreads();
-
-    const uint32_t A = s_count, R1 = 2 * p.IB, KB1 = p.KB1, IB = p.IB, DB = p.DB, K2 = A * IB;
-    const uint32_t total1 = A * R1 * KB1, total2 = DB * K2;
+    const uint32_t A = z.A, R1 = 2 * p.IB, KB1 = p.KB1, IB = p.IB, DB = p.DB;
+    const uint32_t total1 = A * R1 * KB1, total2 = A * DB * IB;
     // CTAs that take part in each phase: as many as there are blocks, so that
     // none between the first and the last of a tile is without one
     const uint32_t G1 = min((uint32_t)G, total1), G2 = min((uint32_t)G, total2);
@@ -255,25 +205,28 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
     uint32_t it = 0;  // the copy thread: blocks whose copies have been started
     bool copier = false;
 
-    if (A == 0) {  // no token has an expert (the same in every CTA)
-        for (int64_t i = (int64_t)cta * THREADS + tid; i < (int64_t)T * p.d; i += (int64_t)G * THREADS)
-            store_y(p.y, p.y_dtype, i, 0.f);
-    } else if (warp == 0) {
+    if (warp == 0) {
         if (elect_one()) {
             copier = true;
             Loader<NT> ld(smem);
-            // A phase's blocks in order: weight tiles from w, in runs of `run`
-            // blocks that follow one another; seek(b) finds block b's tile and
-            // what is left of its run.  The token tiles, `xs_` of them in turn
-            // from `x`, exist once `bar` completes.
-            auto phase = [&](uint32_t b, uint32_t n, uint64_t *bar, auto seek, const uint8_t *x, uint32_t xs_) {
-                const uint32_t ahead = LOCAL ? n : min(n, (uint32_t)STAGES);
+            // A phase's blocks in order, R rows of KT blocks for each expert: the
+            // weight tiles from w; the token tiles from x (each expert's KT of them
+            // for every row) exist once `bar` completes.
+            auto phase = [&](uint32_t b, uint32_t n, uint64_t *bar, const uint8_t *weights, const uint8_t *x, uint32_t R,
+                             uint32_t KT) {
+                const uint32_t ahead = LOCAL ? n : min(n, (uint32_t)STAGES), per = R * KT;
                 Loader<NT> lx = ld;
                 const uint8_t *w = nullptr;
-                uint32_t left = 0;
+                uint32_t a = b / per, left = 0, bytes = 0;
                 auto load = [&](uint32_t i) {
-                    if (left == 0) seek(b + i, w, left);
-                    if (!pipe_load<NT, LOCAL>(pipe, ld, w, LOCAL ? 0 : NT * 128, p.err)) return false;
+                    if (left == 0) {
+                        const uint32_t k = i == 0 ? b - a * per : 0;
+                        if (i) ++a;
+                        w = weights + ((int64_t)z.list[a] * per + k) * GLQ_FP8_TILE_BYTES;
+                        left = per - k;
+                        if (!LOCAL) bytes = (uint32_t)(z.roff[a + 1] - z.roff[a]) * 128;
+                    }
+                    if (!pipe_load<NT, LOCAL>(pipe, ld, w, bytes, p.err)) return false;
                     w += GLQ_FP8_TILE_BYTES;
                     --left;
                     ++it;
@@ -285,34 +238,26 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
                 if (LOCAL) return true;
                 if (!pipe.wait(bar, 0, p.err)) return false;
                 fence_proxy_async();
-                uint32_t xi = b % xs_;
+                uint32_t xa = b / per, xk = (b - xa * per) % KT, xleft = per - (b - xa * per);
+                uint32_t xbytes = (uint32_t)(z.roff[xa + 1] - z.roff[xa]) * 128;
+                const uint8_t *xe = x + (int64_t)z.roff[xa] * KT * 128, *xp = xe + xk * xbytes;
                 for (uint32_t i = 0; i < n; ++i) {
                     if (i >= ahead && !load(i)) return false;
-                    bulk_g2s(lx.dst + GLQ_FP8_TILE_BYTES, x + (int64_t)xi * (NT * 128), NT * 128, &pipe.full[lx.stage]);
-                    if (++xi == xs_) xi = 0;
+                    bulk_g2s(lx.dst + GLQ_FP8_TILE_BYTES, xp, xbytes, &pipe.full[lx.stage]);
                     lx.next();
+                    xp += xbytes;
+                    if (++xk == KT) xk = 0, xp = xe;
+                    if (--xleft == 0 && i + 1 < n) {
+                        ++xa;
+                        xleft = per;
+                        xbytes = (uint32_t)(z.roff[xa + 1] - z.roff[xa]) * 128;
+                        xe = xp = x + (int64_t)z.roff[xa] * KT * 128;
+                    }
                 }
                 return true;
             };
-            // (an expert's gate and up tiles, and a row block of its down tiles,
-            // lie in the order of the blocks)
-            const bool ok = phase(
-                b1, n1, &grid_bar[0],
-                [&](uint32_t b, const uint8_t *&w, uint32_t &left) {
-                    const uint32_t per = R1 * KB1, a = b / per, k = b - a * per;
-                    w = p.w13 + ((int64_t)list[a] * per + k) * GLQ_FP8_TILE_BYTES;
-                    left = per - k;
-                },
-                p.xq, KB1);
-            if (ok)
-                phase(
-                    b2, n2, &grid_bar[2],
-                    [&](uint32_t b, const uint8_t *&w, uint32_t &left) {
-                        const uint32_t rt = b / K2, k = b - rt * K2, a = k / IB, ib = k - a * IB;
-                        w = p.w2 + (((int64_t)list[a] * DB + rt) * IB + ib) * GLQ_FP8_TILE_BYTES;
-                        left = IB - ib;
-                    },
-                    p.hq, K2);
+            if (n1 == 0 || phase(b1, n1, &bars.grid[0], p.w13, p.xq, R1, KB1))
+                if (n2) phase(b2, n2, &bars.grid[2], p.w2, p.hq, DB, IB);
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -322,9 +267,9 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
         }
     } else if (warp == GRID_WARP) {
         if (lane == 0) {
-            uint64_t *const mine[4] = {nullptr, &part1, &formed, &part2};
+            uint64_t *const mine[4] = {&bars.part0, &bars.part1, &bars.formed, &bars.part2};
             for (int n = LOCAL ? 1 : 0; n < 4; n += LOCAL ? 2 : 1) {
-                if (mine[n] && !pipe.wait(mine[n], 0, p.err)) break;
+                if (!pipe.wait(mine[n], 0, p.err)) break;
                 // release: what this CTA's warps wrote before they arrived
                 const uint64_t old = atom_add_u64(p.bar, 1);
                 const uint64_t target = (old / G + 1) * G;  // every call adds a multiple of G
@@ -335,55 +280,93 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
                     else if (sm100::clock_cycles() - t0 > WAIT_CYCLES) pipe.fail(p.err), ok = false;
                 }
                 if (!ok) break;
-                sm100::mbar_arrive(&grid_bar[n]);
+                sm100::mbar_arrive(&bars.grid[n]);
             }
         }
     } else {
-        // One warp: four columns per lane of h of token t for expert a (its place
-        // among those in use; s = t K + which of t's choices), group ib.
-        auto expert_h = [&](uint32_t a, int s, int t, int ib, float (&h)[4]) {
-            float4 v[2], more[2];
-            int c0[2], c1[2];
-            const float *spill = p.spill + (int64_t)t * 128 + lane * 4;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {  // gate, up: every load before the first sum
-                const uint32_t r = 2 * ib + g, first = (a * R1 + r) * KB1;
-                c0[g] = range_owner(first, total1, G1), c1[g] = range_owner(first + KB1 - 1, total1, G1);
-                v[g] = __ldcg(reinterpret_cast<const float4 *>(p.main + ((int64_t)s * R1 + r) * 128 + lane * 4));
-                more[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c1[g] > c0[g]) more[g] = __ldcg(reinterpret_cast<const float4 *>(spill + (int64_t)(c0[g] + 1) * NT * 128));
+        // x^: a warp per token and group, into the tiles of the token's experts
+        auto form_x = [&]() {
+            for (int i = (warp - X_WARP0) * G + cta; i < T * (int)KB1; i += H_WARPS * G) {
+                const int t = i / (int)KB1, kb = i - t * (int)KB1, col = kb * GLQ_FP8_BLOCK + lane * 4;
+                uint2 w = make_uint2(0, 0);  // d is a multiple of 8: a lane's four columns are in or out together
+                if (col < p.d)
+                    w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.d + col));
+                const float2 a = p.x_dtype ? unpack2<__nv_bfloat16>(w.x) : unpack2<__half>(w.x);
+                const float2 b = p.x_dtype ? unpack2<__nv_bfloat16>(w.y) : unpack2<__half>(w.y);
+                const float v[4] = {a.x, a.y, b.x, b.y};
+                float s;
+                const uint32_t q = warp_quantize(v, s);
+                for (int c = 0; c < K; ++c) {
+                    const int e = z.ids[t * K + c];
+                    if (e < 0) continue;
+                    const uint32_t r = z.rank[e], ro = z.roff[r], rows = z.roff[r + 1] - ro;
+                    uint8_t *tile = p.xq + ((int64_t)ro * KB1 + kb * rows) * 128;
+                    __stcg(reinterpret_cast<uint32_t *>(tile + sw128(z.place(e, t), lane >> 2)) + (lane & 3), q);
+                }
+                if (lane == 0) __stcg(p.xs + kb * T + t, s);
             }
+            fence_proxy_async();  // x^ is read by bulk copies
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&bars.part0);
+        };
+        // One warp: four columns per lane of h, group ib of the expert with place a,
+        // for the token with place j among its own (s = t K + which of t's
+        // choices).  The loads, and their sum:
+        struct Sums {
+            float4 v[2], more[2];  // gate, up
+        };
+        auto owners = [&](uint32_t a, int ib) {  // lanes 0 to 3: the CTAs with the first and last blocks of both tiles
+            return range_owner((a * R1 + 2 * ib + ((lane >> 1) & 1)) * KB1 + (lane & 1 ? KB1 - 1 : 0), total1, G1);
+        };
+        auto load_h = [&](int owner, int s, int j, int ib) {
+            Sums m;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                v[g] = add4(v[g], more[g]);
-#pragma unroll 4
-                for (int c = c0[g] + 2; c <= c1[g]; ++c)
-                    v[g] = add4(v[g], __ldcg(reinterpret_cast<const float4 *>(spill + (int64_t)c * NT * 128)));
+                const int c0 = __shfl_sync(0xffffffffu, owner, 2 * g), c1 = __shfl_sync(0xffffffffu, owner, 2 * g + 1);
+                m.v[g] = __ldcg(reinterpret_cast<const float4 *>(p.main1 + ((int64_t)s * R1 + 2 * ib + g) * 128 + lane * 4));
+                m.more[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c1 > c0)
+                    m.more[g] = __ldcg(reinterpret_cast<const float4 *>(p.spill1 + ((int64_t)(c0 + 1) * NT + j) * 128 + lane * 4));
             }
-            h[0] = silu(v[0].x) * v[1].x;
-            h[1] = silu(v[0].y) * v[1].y;
-            h[2] = silu(v[0].z) * v[1].z;
-            h[3] = silu(v[0].w) * v[1].w;
+            return m;
+        };
+        auto finish_h = [&](Sums &m, int owner, int j, float (&h)[4]) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int c0 = __shfl_sync(0xffffffffu, owner, 2 * g), c1 = __shfl_sync(0xffffffffu, owner, 2 * g + 1);
+                m.v[g] = add4(m.v[g], m.more[g]);
+#pragma unroll 4
+                for (int c = c0 + 2; c <= c1; ++c)
+                    m.v[g] = add4(m.v[g], __ldcg(reinterpret_cast<const float4 *>(p.spill1 + ((int64_t)c * NT + j) * 128 + lane * 4)));
+            }
+            h[0] = silu(m.v[0].x) * m.v[1].x;
+            h[1] = silu(m.v[0].y) * m.v[1].y;
+            h[2] = silu(m.v[0].z) * m.v[1].z;
+            h[3] = silu(m.v[0].w) * m.v[1].w;
         };
         // h^: a warp per (token, choice) and group of the expert's width
         auto form = [&]() {
-            if (!pipe.wait_warp(&grid_bar[1], 0, p.err)) return false;
+            if (!pipe.wait_warp(&bars.grid[1], 0, p.err)) return false;
             for (int i = (warp - X_WARP0) * G + cta; i < T * K * (int)IB; i += H_WARPS * G) {
-                const int s = i / (int)IB, ib = i - s * (int)IB, e = ids[s], t = s / K;
+                const int s = i / (int)IB, ib = i - s * (int)IB, e = z.ids[s];
                 if (e < 0) continue;
-                const uint32_t a = rank[e];
+                const uint32_t a = z.rank[e], ro = z.roff[a], rows = z.roff[a + 1] - ro;
+                const int j = z.place(e, s / K);
                 float h[4], sc;
-                expert_h(a, s, t, ib, h);
+                const int owner = owners(a, ib);
+                Sums m = load_h(owner, s, j, ib);
+                finish_h(m, owner, j, h);
                 const uint32_t q = warp_quantize(h, sc);
-                const int64_t tile = (int64_t)a * IB + ib;
-                __stcg(reinterpret_cast<uint32_t *>(p.hq + tile * (NT * 128) + sw128(t, lane >> 2)) + (lane & 3), q);
-                if (lane == 0) __stcg(p.hs + tile * NT + t, sc * wts[s]);
+                const int64_t row0 = (int64_t)ro * IB + ib * rows;
+                __stcg(reinterpret_cast<uint32_t *>(p.hq + row0 * 128 + sw128(j, lane >> 2)) + (lane & 3), q);
+                if (lane == 0) __stcg(p.hs + row0 + j, sc * z.wts[s]);
             }
             fence_proxy_async();  // h^ is read by bulk copies
             __syncwarp();
-            if (lane == 0) sm100::mbar_arrive(&formed);
+            if (lane == 0) sm100::mbar_arrive(&bars.formed);
             return true;
         };
+        if constexpr (!LOCAL) form_x();
         if (warp < D_WARP0) {
             // ---------------- scales ----------------
             constexpr int SC = (NT + 31) / 32;
@@ -398,65 +381,82 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
             };
             // the block scales come from DRAM, behind the weights in flight: into L2
             // before those are too many
-            for (uint32_t j = (w0 * 32 + lane) * 32; j < n1; j += X_WARPS * 32 * 32) {
-                const uint32_t b = b1 + j, a = b / (R1 * KB1);
-                prefetch_l2(p.s13 + (int64_t)list[a] * (R1 * KB1) + (b - a * (R1 * KB1)));
-            }
-            for (uint32_t j = w0 * 32 + lane; j < n2; j += X_WARPS * 32) {
-                const uint32_t b = b2 + j, rt = b / K2, k = b - rt * K2, a = k / IB;
-                prefetch_l2(p.s2 + ((int64_t)list[a] * DB + rt) * IB + (k - a * IB));
-            }
-            bool ok = LOCAL || pipe.wait_warp(&grid_bar[0], 0, p.err);
+            auto prefetch = [&](const float *scales, uint32_t b, uint32_t n, uint32_t per) {
+                for (uint32_t j = (w0 * 32 + lane) * 32; j < n; j += X_WARPS * 32 * 32) {
+                    const uint32_t a = (b + j) / per;
+                    prefetch_l2(scales + (int64_t)z.list[a] * per + (b + j - a * per));
+                }
+            };
+            const uint32_t per1 = R1 * KB1, per2 = DB * IB;
+            prefetch(p.s13, b1, n1, per1);
+            prefetch(p.s2, b2, n2, per2);
+            bool ok = LOCAL || pipe.wait_warp(&bars.grid[0], 0, p.err);
             uint32_t i = w0;
             if (w0 >= turn) i = n1 + n2;
             for (; ok && i < n1; i += turn) {
-                const uint32_t b = b1 + i, a = b / (R1 * KB1), kb = b % KB1;
-                const float ws = __ldg(p.s13 + (int64_t)list[a] * (R1 * KB1) + (b - a * (R1 * KB1)));
+                const uint32_t b = b1 + i, a = b / per1, kb = b % KB1;
+                const float ws = __ldg(p.s13 + (int64_t)z.list[a] * per1 + (b - a * per1));
+                const int o = z.off[a], live = z.off[a + 1] - o;
                 if constexpr (LOCAL) {
                     const int col = kb * GLQ_FP8_BLOCK + lane * 4;
                     uint2 w[LOCAL_T];
 #pragma unroll
-                    for (int t = 0; t < LOCAL_T; ++t) {
-                        w[t] = make_uint2(0, 0);
-                        if (t < T && col < p.d)
-                            w[t] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.d + col));
+                    for (int j = 0; j < LOCAL_T; ++j) {
+                        w[j] = make_uint2(0, 0);
+                        if (j < live && col < p.d)
+                            w[j] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.x) +
+                                                                         (int64_t)(z.pairs[o + j] >> 4) * p.d + col));
                     }
-                    ok = p.x_dtype ? put_rounded<NT, __nv_bfloat16>(pipe, smem, i, w, T, ws, lane, p.err)
-                                   : put_rounded<NT, __half>(pipe, smem, i, w, T, ws, lane, p.err);
+                    ok = p.x_dtype ? put_rounded<NT, __nv_bfloat16>(pipe, smem, i, w, live, ws, lane, p.err)
+                                   : put_rounded<NT, __half>(pipe, smem, i, w, live, ws, lane, p.err);
                 } else {
                     float s[SC];
 #pragma unroll
-                    for (int j = 0; j < SC; ++j)
-                        s[j] = j * 32 + lane < T ? __ldcg(p.xs + kb * NT + j * 32 + lane) * ws : 0.f;
+                    for (int j = 0; j < SC; ++j) {
+                        const int at_j = j * 32 + lane;
+                        s[j] = at_j < live ? __ldcg(p.xs + kb * T + (z.pairs[o + at_j] >> 4)) * ws : 0.f;
+                    }
                     ok = put(i, s);
                 }
             }
-            if constexpr (LOCAL) ok = ok && pipe.wait_warp(&grid_bar[1], 0, p.err);
-            else ok = ok && form() && pipe.wait_warp(&grid_bar[2], 0, p.err);
+            if constexpr (LOCAL) ok = ok && pipe.wait_warp(&bars.grid[1], 0, p.err);
+            else ok = ok && form() && pipe.wait_warp(&bars.grid[2], 0, p.err);
             for (; ok && i < n1 + n2; i += turn) {
-                const uint32_t b = b2 + (i - n1), rt = b / K2, k = b - rt * K2, a = k / IB, ib = k - a * IB;
-                const float ws = __ldg(p.s2 + ((int64_t)list[a] * DB + rt) * IB + ib);
+                const uint32_t b = b2 + (i - n1), a = b / per2, ib = b % IB;
+                const float ws = __ldg(p.s2 + (int64_t)z.list[a] * per2 + (b - a * per2));
+                const int o = z.off[a], live = z.off[a + 1] - o;
                 float s[SC];
                 if constexpr (LOCAL) {
+                    const int owner = owners(a, ib);
+                    auto choice = [&](int j) {
+                        const int pair = z.pairs[o + j];
+                        return (pair >> 4) * K + (pair & 15);
+                    };
+                    int c = choice(0);
+                    Sums m = load_h(owner, c, 0, ib);
                     if (!(ok = pipe_x_begin(pipe, i, p.err))) break;
                     uint8_t *xt = pipe_x_tile<NT>(smem, i);
                     s[0] = 0.f;
 #pragma unroll 1
-                    for (int t = 0; t < T; ++t) {  // rolled: it runs a few times a call, from a cold instruction cache
-                        const uint8_t c = slot[a * NT + t];
-                        if (c == NONE) continue;
+                    for (int j = 0; j < live; ++j) {  // rolled: it runs a few times a call, from a cold instruction cache
+                        const int next = choice(min(j + 1, live - 1));
+                        Sums ahead = m;
+                        if (j + 1 < live) ahead = load_h(owner, next, j + 1, ib);
                         float h[4], sc;
-                        expert_h(a, t * K + c, t, ib, h);
-                        *reinterpret_cast<uint32_t *>(xt + sw128(t, lane >> 2) + (lane & 3) * 4) = warp_quantize(h, sc);
-                        if (lane == t) s[0] = sc * wts[t * K + c] * ws;
+                        finish_h(m, owner, j, h);
+                        *reinterpret_cast<uint32_t *>(xt + sw128(j, lane >> 2) + (lane & 3) * 4) = warp_quantize(h, sc);
+                        if (lane == j) s[0] = sc * z.wts[c] * ws;
+                        m = ahead, c = next;
                     }
                     if (lane < NT) pipe.sc[i % STAGES][lane] = s[0];
                     pipe_x_done<NT, true>(pipe, i, lane);
                 } else {
+                    const uint32_t ro = z.roff[a], rows = z.roff[a + 1] - ro;
+                    const float *hs = p.hs + (int64_t)ro * IB + ib * rows;
 #pragma unroll
                     for (int j = 0; j < SC; ++j) {
-                        const int t = j * 32 + lane;
-                        s[j] = t < T && slot[a * NT + t] != NONE ? __ldcg(p.hs + (int64_t)k * NT + t) * ws : 0.f;
+                        const int at_j = j * 32 + lane;
+                        s[j] = at_j < live ? __ldcg(hs + at_j) * ws : 0.f;
                     }
                     ok = put(i, s);
                 }
@@ -464,84 +464,221 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
         } else {
             // ---------------- drain ----------------
             const int quadrant = warp & 3, set = (warp - D_WARP0) >> 2;
-            const int row = 32 * quadrant + lane, dtid = tid - D_WARP0 * 32;
+            const int row = 32 * quadrant + lane;
             float acc[HALF];
             uint32_t i = 0;
             bool ok = true;
-            // Phase 0: sums per (token, expert); the piece with a tile's first block
-            // in `main`, a CTA's piece of an earlier CTA's tile in `spill`.  Phase
-            // 1: sums per token; a CTA's piece of a split tile in `part`.
-            auto phase = [&](auto skip, int ph) {
-                constexpr bool SKIP = decltype(skip)::value;
-                const uint32_t end = ph ? n1 + n2 : n1, KT = ph ? K2 : KB1, b = ph ? b2 : b1;
+            // Sums per (token, expert) and row tile; the piece with a tile's first
+            // block in `main`, a CTA's piece of an earlier CTA's tile in `spill`.
+            auto phase = [&](uint32_t b, uint32_t end, uint32_t R, uint32_t KT, float *main, float *spill) {
                 uint32_t tile = b / KT, k = b - tile * KT;
                 while (ok && i < end) {
-                    const uint32_t len = min(KT - k, end - i);
+                    const uint32_t len = min(KT - k, end - i), a = tile / R, r = tile - a * R;
+                    const int o = z.off[a], live = z.off[a + 1] - o;
 #pragma unroll
                     for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
                     for (uint32_t n = 0; ok && n < len;) {
                         const bool two = DRAIN == 2 && n + 2 <= len;
-                        ok = two ? pipe_drain<NT, DRAIN, SKIP>(pipe, i, quadrant, set, acc, p.err)
-                                 : pipe_drain<NT, 1, SKIP>(pipe, i, quadrant, set, acc, p.err);
+                        ok = two ? pipe_drain<NT, DRAIN>(pipe, i, quadrant, set, acc, p.err)
+                                 : pipe_drain<NT, 1>(pipe, i, quadrant, set, acc, p.err);
                         n += two ? 2 : 1;
                         i += two ? 2 : 1;
                     }
                     if (!ok) break;
-                    const uint32_t a = tile / R1, r = tile - a * R1;   // phase 0
-                    const bool whole = k == 0 && len == KT;            // phase 1
-                    const int64_t col = (int64_t)tile * 128 + row;
-                    float *part = p.part + ((int64_t)cta * 2 + (k == 0 ? 1 : 0)) * NT * 128 + row;
 #pragma unroll
                     for (int j = 0; j < HALF; ++j) {
-                        const int t = set * HALF + j;
-                        if (t >= T) continue;
-                        if (ph == 0) {
-                            const uint8_t c = slot[a * NT + t];
-                            if (c != NONE)
-                                __stcg(k == 0 ? p.main + (((int64_t)t * K + c) * R1 + r) * 128 + row
-                                              : p.spill + ((int64_t)cta * NT + t) * 128 + row, acc[j]);
-                        } else if (!whole) {
-                            __stcg(part + t * 128, acc[j]);
-                        } else if (col < p.d) {
-                            store_y(p.y, p.y_dtype, (int64_t)t * p.d + col, acc[j]);
-                        }
+                        const int at_j = set * HALF + j;
+                        if (at_j >= live) break;
+                        const int at_p = z.pairs[o + at_j];
+                        __stcg(k == 0 ? main + ((int64_t)((at_p >> 4) * K + (at_p & 15)) * R + r) * 128 + row
+                                      : spill + ((int64_t)cta * NT + at_j) * 128 + row, acc[j]);
                     }
                     ++tile;
                     k = 0;
                 }
             };
-            phase(std::false_type{}, 0);
+            phase(b1, n1, R1, KB1, p.main1, p.spill1);
             __syncwarp();
-            if (ok && lane == 0) sm100::mbar_arrive(&part1);
+            if (ok && lane == 0) sm100::mbar_arrive(&bars.part1);
             if (!LOCAL) ok = ok && form();
-            phase(std::true_type{}, 1);
+            phase(b2, n1 + n2, DB, IB, p.main2, p.spill2);
             __syncwarp();
-            if (ok && lane == 0) sm100::mbar_arrive(&part2);
-            ok = ok && pipe.wait_warp(&grid_bar[3], 0, p.err);
-            // the tiles that were split: four columns of one token per thread
-            for (int j = cta * (D_WARPS * 32) + dtid; ok && j < T * (int)DB * 32; j += G * D_WARPS * 32) {
-                const int t = j / ((int)DB * 32), c4 = j - t * ((int)DB * 32), rt = c4 >> 5, col = c4 * 4;
-                const uint32_t first = rt * K2;
-                const int c0 = range_owner(first, total2, G2), c1 = range_owner(first + K2 - 1, total2, G2);
-                if (c0 == c1 || col >= p.d) continue;
-                const int64_t off = (int64_t)t * 128 + (c4 & 31) * 4;
-                float4 sum = __ldcg(reinterpret_cast<const float4 *>(p.part + ((int64_t)c0 * 2 + 1) * NT * 128 + off));
-#pragma unroll 4
-                for (int c = c0 + 1; c <= c1; ++c)
-                    sum = add4(sum, __ldcg(reinterpret_cast<const float4 *>(p.part + (int64_t)c * 2 * NT * 128 + off)));
-                store_y4(p.y, p.y_dtype, (int64_t)t * p.d + col, sum);
+            if (ok && lane == 0) sm100::mbar_arrive(&bars.part2);
+            // y: a warp per token and 128 columns
+            const int u0 = (warp - D_WARP0) * G + cta;
+            for (int u = u0; ok && u < T * (int)DB; u += D_WARPS * G) {
+                const int t = u / (int)DB, rt = u - t * (int)DB, col = rt * 128 + lane * 4;
+                // lane c: choice c's pieces, and how many there are before them
+                const int e = lane < K ? z.ids[t * K + lane] : -1;
+                int c0 = 0, n = 0, at_j = 0;
+                if (e >= 0) {
+                    const uint32_t first = ((uint32_t)z.rank[e] * DB + rt) * IB;
+                    c0 = range_owner(first, total2, G2), n = range_owner(first + IB - 1, total2, G2) - c0 + 1;
+                    at_j = z.place(e, t);
+                }
+                int end = n;
+#pragma unroll
+                for (int d = 1; d < MOE_MAX_K; d <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, end, d);
+                    if (lane >= d) end += v;
+                }
+                const int pieces = __shfl_sync(0xffffffffu, end, MOE_MAX_K - 1);
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int base = 0; base < pieces || (base == 0 && u == u0); base += 32) {
+                    // lane l: where piece base + l is, beside its columns
+                    const float *from = p.main2;
+                    for (int c = 0; c < K; ++c) {
+                        const int ce = __shfl_sync(0xffffffffu, end, c), cn = __shfl_sync(0xffffffffu, n, c);
+                        const int cc = __shfl_sync(0xffffffffu, c0, c), cj = __shfl_sync(0xffffffffu, at_j, c);
+                        const int o = base + lane - (ce - cn);  // which of choice c's pieces
+                        if (o == 0 && cn) from = p.main2 + ((int64_t)(t * K + c) * DB + rt) * 128;
+                        if (o > 0 && o < cn) from = p.spill2 + ((int64_t)(cc + o) * NT + cj) * 128;
+                    }
+                    if (base == 0 && u == u0 && !(ok = pipe.wait_warp(&bars.grid[3], 0, p.err))) break;
+                    const int here = min(32, pieces - base);
+                    constexpr int Q = 8;  // loads in flight
+                    for (int l = 0; l < here; l += Q) {
+                        float4 v[Q];
+#pragma unroll
+                        for (int q = 0; q < Q; ++q) {
+                            const float *at_l = reinterpret_cast<const float *>(
+                                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), (l + q) & 31));
+                            v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (l + q < here) v[q] = __ldcg(reinterpret_cast<const float4 *>(at_l + lane * 4));
+                        }
+#pragma unroll
+                        for (int q = 0; q < Q; ++q) sum = add4(sum, v[q]);
+                    }
+                }
+                if (!ok) break;
+                if (col < p.d) store_y4(p.y, p.y_dtype, (int64_t)t * p.d + col, sum);
             }
         }
     }
     // converged, or a warp whose one thread is still at work counts twice
     __syncwarp();
-    sm100::tc_fence_before();
     __syncthreads();
     if (copier && pipe.abort) pipe_load_drain(pipe, it);
     __syncwarp();
+}
+
+union PipeSpace {  // one of them is used
+    Pipe<16> few;
+    Pipe<32> some;
+    Pipe<64> many;
+    __device__ PipeSpace() {}
+};
+constexpr size_t ring_bytes(int max_nt) {
+    const size_t few = (size_t)Pipe<16>::STAGES * Pipe<16>::STAGE_BYTES, some = (size_t)Pipe<32>::STAGES * Pipe<32>::STAGE_BYTES,
+                 many = (size_t)Pipe<64>::STAGES * Pipe<64>::STAGE_BYTES;
+    return max_nt == 16 ? few : few > some ? (few > many ? few : many) : some > many ? some : many;
+}
+
+// LOCAL (at most LOCAL_T tokens): x^ and h^ are not shared through memory;
+// every CTA rounds the tokens' columns that its own blocks need into its
+// operand tiles.  The work is done several times over, but two of the four
+// barriers, 2 to 4 us each while the weights saturate the memory, and h's trip
+// through memory go.
+//
+// The body's NT is the smallest that holds the tokens of every expert; 64
+// tokens rarely bring one expert more than 16.  A stage is then 18 KB instead
+// of 24 and there are 11 instead of 7 (179 -> 148 us, as above).
+// LOCAL_T: 4 tokens of 128 experts of 2048 x 768 took 38 us (LOCAL) and 42 us,
+// 8 tokens of 32 experts of 4096 x 2048 111 us and 101 us.
+template <int MAX_NT, bool LOCAL>
+__global__ void __launch_bounds__(THREADS, 1) moe_kernel(MoeParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(16) PipeSpace pipe_space;
+    __shared__ uint32_t tmem;
+    __shared__ Barriers bars;
+    __shared__ int s_count, s_most;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = blockIdx.x, G = gridDim.x;
+    const int T = p.T, E = p.E, K = p.k;
+    const Layout at = layout_of((uint32_t)ring_bytes(MAX_NT), T, E, K);
+    Routing z;
+    z.mask = reinterpret_cast<unsigned long long *>(smem + at.mask);
+    z.wts = reinterpret_cast<float *>(smem + at.wts);
+    z.rank = reinterpret_cast<int16_t *>(smem + at.rank), z.list = reinterpret_cast<int16_t *>(smem + at.list);
+    z.ids = reinterpret_cast<int16_t *>(smem + at.ids);
+    z.off = reinterpret_cast<uint16_t *>(smem + at.off), z.roff = reinterpret_cast<uint16_t *>(smem + at.roff);
+    z.pairs = reinterpret_cast<uint16_t *>(smem + at.pairs);
+
+    // ---------------- setup, routing ----------------
+    if (MAX_NT == 16 && warp == 2) pipe_space.few.init(lane, 1);
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(&bars.grid[i], 1);
+        mbar_init(&bars.part0, H_WARPS);
+        mbar_init(&bars.part1, D_WARPS);
+        mbar_init(&bars.formed, H_WARPS);
+        mbar_init(&bars.part2, D_WARPS);
+    }
+    if (warp == 1) {
+        sm100::tmem_alloc(MAX_NT == 16 ? &pipe_space.few.tmem : &tmem, MAX_NT == 16 ? 256 : 512);
+        sm100::tmem_relinquish();
+    }
+    for (int e = tid; e < E; e += THREADS) z.mask[e] = 0;
+    if (tid == 0) prefetch_l2(p.bar);  // before the weights are in flight
+    __syncthreads();
+    for (int t = warp; t < T; t += WARPS) {
+        if (E <= 128) route<4>(p, t, lane, z.ids + t * K, z.wts + t * K, z.mask);
+        else route<16>(p, t, lane, z.ids + t * K, z.wts + t * K, z.mask);
+    }
+    sm100::tc_fence_before();
+    __syncthreads();
+    sm100::tc_fence_after();
+    if (warp == 0) {  // experts in use, in order, and where their tokens begin
+        const int per = (E + 31) / 32, e0 = lane * per, e1 = min(E, e0 + per);  // a lane's experts
+        int used = 0, sum = 0, most = 0;  // sum: tokens, and tokens rounded up to 8 in the upper half
+        for (int e = e0; e < e1; ++e) {
+            const int c = __popcll(z.mask[e]);
+            used += c != 0, sum += c | ((c + 7) & ~7) << 16;
+            if (MAX_NT > 16) most = max(most, c);
+        }
+        int n = used, o = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, n, d), b = __shfl_up_sync(0xffffffffu, o, d);
+            if (lane >= d) n += a, o += b;
+        }
+        if (MAX_NT > 16) most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 31) s_count = n, s_most = most, z.off[n] = (uint16_t)(o & 0xFFFF), z.roff[n] = (uint16_t)(o >> 16);
+        n -= used, o -= sum;  // of the lanes before
+        for (int e = e0; used && e < e1; ++e) {
+            const int c = __popcll(z.mask[e]);
+            if (c == 0) continue;
+            z.rank[e] = (int16_t)n;
+            z.list[n] = (int16_t)e;
+            z.off[n] = (uint16_t)(o & 0xFFFF), z.roff[n] = (uint16_t)(o >> 16);
+            ++n, o += c | ((c + 7) & ~7) << 16;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < T * K; i += THREADS) {
+        const int e = z.ids[i], t = i / K;
+        if (e >= 0) z.pairs[z.off[z.rank[e]] + z.place(e, t)] = (uint16_t)(t * 16 + (i - t * K));
+    }
+    __syncthreads();
+
+    z.A = s_count;
+    if (z.A == 0) {  // no token has an expert (the same in every CTA)
+        for (int64_t i = (int64_t)cta * THREADS + tid; i < (int64_t)T * p.d; i += (int64_t)G * THREADS)
+            store_y(p.y, p.y_dtype, i, 0.f);
+    } else if constexpr (MAX_NT == 16) {
+        moe_body<16, MAX_NT, LOCAL>(p, z, bars, pipe_space.few, smem, tmem);
+    } else if (s_most <= 16) {
+        moe_body<16, MAX_NT, LOCAL>(p, z, bars, pipe_space.few, smem, tmem);
+    } else if (s_most <= 32) {
+        moe_body<32, MAX_NT, LOCAL>(p, z, bars, pipe_space.some, smem, tmem);
+    } else {
+        moe_body<64, MAX_NT, LOCAL>(p, z, bars, pipe_space.many, smem, tmem);
+    }
+    sm100::tc_fence_before();
+    __syncthreads();
     if (warp == 1) {
         sm100::tc_fence_after();
-        sm100::tmem_dealloc(pipe.tmem, P::TMEM_COLS);
+        sm100::tmem_dealloc(MAX_NT == 16 ? pipe_space.few.tmem : tmem, MAX_NT == 16 ? 256 : 512);
     }
 }
 
@@ -551,23 +688,20 @@ struct MoeKernel {
     int key;
 };
 
-template <int NT, bool LOCAL>
+template <int MAX_NT, bool LOCAL>
 MoeKernel moe_kernel_of(const MoeParams &p, int key) {
-    return {(const void *)moe_kernel<NT, LOCAL>,
-            1024 + layout_of(Pipe<NT>::STAGES * Pipe<NT>::STAGE_BYTES, NT, p.T, p.E, p.k).end, key};
+    return {(const void *)moe_kernel<MAX_NT, LOCAL>, 1024 + layout_of((uint32_t)ring_bytes(MAX_NT), p.T, p.E, p.k).end, key};
 }
 
 }  // namespace
 
-int moe_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+int moe_tile(int T) { return T <= 16 ? 16 : 64; }
 
 cudaError_t launch_moe(const MoeParams &p, int grid, cudaStream_t s) {
-    const int nt = moe_tile(p.T);
-    const MoeKernel k = p.T <= LOCAL_T ? moe_kernel_of<16, true>(p, 0)
-                        : nt == 16     ? moe_kernel_of<16, false>(p, 1)
-                        : nt == 32     ? moe_kernel_of<32, false>(p, 2)
-                                       : moe_kernel_of<64, false>(p, 3);
-    static std::atomic<uint64_t> configured[4];
+    const MoeKernel k = p.T <= LOCAL_T          ? moe_kernel_of<16, true>(p, 0)
+                        : moe_tile(p.T) == 16 ? moe_kernel_of<16, false>(p, 1)
+                                              : moe_kernel_of<64, false>(p, 2);
+    static std::atomic<uint64_t> configured[3];
     const cudaError_t e = once_per_device(configured[k.key], [&k] {
         return cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, MOE_SMEM_LIMIT);
     });
