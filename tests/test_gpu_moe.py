@@ -152,6 +152,21 @@ def test_one_expert_for_all(glq):
     ex.check(layer(x.cuda(), logits.cuda()), x, logits, 1)
 
 
+@pytest.mark.parametrize("fullest", [15, 16, 17, 32, 33, 63])
+def test_fullest_expert(glq, fullest):
+    """One expert with a given number of the 64 tokens beside many with a few: every token tile, full and one over."""
+    gen = torch.Generator().manual_seed(38)
+    ex = Experts(gen, 48, 264, 136)
+    layer = ex.layer(glq, 2)
+    x, logits = _inputs(gen, 64, 48, 264, torch.bfloat16)
+    logits[:, 7] = -float("inf")
+    logits[torch.randperm(64, generator=gen)[:fullest], 7] = 9.0
+    chosen = torch.bincount(torch.topk(logits, 2).indices.flatten(), minlength=48)
+    assert chosen[7] == fullest and chosen.sort().values[-2] < 15
+    ex.check(layer(x.cuda(), logits.cuda()), x, logits, 2)
+    layer.check()
+
+
 def test_streams_graphs_and_reservation(glq):
     gen = torch.Generator().manual_seed(36)
     ex = Experts(gen, 16, 264, 136)
