@@ -173,11 +173,12 @@ __global__ void __launch_bounds__(256) fp8_dequant_kernel(const uint8_t *tiles, 
 // (Parts through global memory, summed by the CTA that arrives last, cost 3.5
 // to 5 us at the end of every call: store, atomic and load each make the trip
 // to L2.)
-// SOURCE 0 / 1: f16 / bf16 activations rounded on the way; 2: e4m3 rows (by
+// SOURCE 0 / 1: f16 / bf16 activations of up to ROWS tokens rounded on the way;
+// 2: e4m3 rows (by
 // TMA: 128 columns x NT tokens, 128-byte swizzle) and their scales.
 // ---------------------------------------------------------------------------
 
-template <int NT, int SOURCE>
+template <int NT, int SOURCE, int ROWS = 1>
 __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __grid_constant__ CUtensorMap qmap,
                                                                      Fp8SkinnyParams p) {
     constexpr bool ROUND = SOURCE != 2;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
         // add its trip to the time a stage takes to come round (0.37 us a
         // block for 11 stages, whatever the number of SMs).
         using T = typename std::conditional<SOURCE == 0, __half, __nv_bfloat16>::type;
-        constexpr int ROWS = ROUND ? FP8_ROUND_MAX : 1, SC = (NT + 31) / 32;
+        constexpr int SC = (NT + 31) / 32;
         struct Ahead {
             uint2 x[ROWS];
             float s[SC], ws;
@@ -444,10 +445,13 @@ struct SkinnyKernel {
     int key;
 };
 
-SkinnyKernel skinny_kernel(int source, int nt) {
-    if (source < 2)  // at most FP8_ROUND_MAX tokens
-        return {source ? (const void *)fp8_skinny_kernel<16, 1> : (const void *)fp8_skinny_kernel<16, 0>,
-                Pipe<16>::SMEM_BYTES, source};
+SkinnyKernel skinny_kernel(int source, int nt, int B) {
+    if (source < 2 && B <= FP8_ROUND_FEW)
+        return {source ? (const void *)fp8_skinny_kernel<16, 1, FP8_ROUND_FEW>
+                       : (const void *)fp8_skinny_kernel<16, 0, FP8_ROUND_FEW>, Pipe<16>::SMEM_BYTES, source};
+    if (source < 2)
+        return {source ? (const void *)fp8_skinny_kernel<16, 1, FP8_ROUND_MAX>
+                       : (const void *)fp8_skinny_kernel<16, 0, FP8_ROUND_MAX>, Pipe<16>::SMEM_BYTES, 5 + source};
     switch (nt) {
         case 16: return {(const void *)fp8_skinny_kernel<16, 2>, Pipe<16>::SMEM_BYTES, 2};
         case 32: return {(const void *)fp8_skinny_kernel<32, 2>, Pipe<32>::SMEM_BYTES, 3};
@@ -457,7 +461,7 @@ SkinnyKernel skinny_kernel(int source, int nt) {
 
 // Sets the kernel's shared memory limit once per device.
 cudaError_t prepare(const SkinnyKernel &k) {
-    static std::atomic<uint64_t> configured[5];
+    static std::atomic<uint64_t> configured[7];
     return once_per_device(configured[k.key], [&k] {
         return cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
     });
@@ -477,7 +481,7 @@ cudaError_t fp8_skinny_clusters(int num_sms, int count[9]) {
         for (int c = 0; c <= 8; ++c) count[c] = known[dev][c];
         return cudaSuccess;
     }
-    const SkinnyKernel k = skinny_kernel(2, 16);
+    const SkinnyKernel k = skinny_kernel(2, 16, 16);
     e = prepare(k);
     count[0] = 0;
     count[1] = num_sms;
@@ -500,6 +504,16 @@ cudaError_t fp8_skinny_clusters(int num_sms, int count[9]) {
         asked[dev].store(true, std::memory_order_release);
     }
     return e;
+}
+
+bool fp8_rounds_inside(int64_t B, int64_t tiles, int KB, int num_sms) {
+    // A launch of the quantiser in front costs about 1.1 us; a block's rounding
+    // inside the kernel comes once per row tile, and from 5 tokens on is slower
+    // than its weights.  Measured, inside against in front: 960x960 at 5 / 8
+    // tokens 4.7 / 4.9 against 5.6 / 5.5 us; 4096x14336 (24 blocks per SM) 14.6 /
+    // 14.9 against 15.5 / 15.4; 32768x5120 (69) 31.9 / 32.8 against 30.6 / 30.5,
+    // but at 4 tokens 29.4 against 30.6; 4096x14336 at 16 tokens 24.4 against 16.
+    return B <= FP8_ROUND_FEW || (B <= FP8_ROUND_MAX && tiles * KB <= (int64_t)32 * num_sms);
 }
 
 Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, int nt, const int clusters[9]) {
@@ -533,7 +547,7 @@ Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, int nt, const int clusters[
 
 cudaError_t launch_fp8_skinny(const Fp8SkinnyParams &p, const CUtensorMap &qmap, int source, int nt, int clusters,
                               cudaStream_t s, bool pdl) {
-    const SkinnyKernel k = skinny_kernel(source, nt);
+    const SkinnyKernel k = skinny_kernel(source, nt, p.B);
     const cudaError_t e = prepare(k);
     if (e != cudaSuccess) return e;
     Fp8SkinnyParams q = p;

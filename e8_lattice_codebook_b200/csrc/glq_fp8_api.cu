@@ -81,9 +81,7 @@ void free_fp8(glq_fp8 L) {
     delete L;
 }
 
-// Batches whose activations the product itself rounds; above, a kernel of
-// their own rounds them first.
-bool rounds_inside(int64_t B) { return B <= glq::FP8_ROUND_MAX; }
+bool rounds_inside(glq_fp8 L, int64_t B) { return glq::fp8_rounds_inside(B, L->RT, L->KB, L->num_sms); }
 
 // The many-token kernel's tiles and parts of K.
 glq::Fp8GemmParams gemm_params(glq_fp8 L, int64_t B) {
@@ -110,7 +108,7 @@ void fp8_need(glq_fp8 L, int64_t B, bool quantized, size_t need[glq::FP8_WS_COUN
             need[glq::FP8_WS_Z] =
                 std::max(need[glq::FP8_WS_Z], (size_t)p.ksplit * p.part_rows * (size_t)L->m * sizeof(float));
     }
-    if (B <= 0 || quantized || rounds_inside(B)) return;
+    if (B <= 0 || quantized || rounds_inside(L, B)) return;
     need[glq::FP8_WS_Q] = std::max(need[glq::FP8_WS_Q], (size_t)B * L->KB * GLQ_FP8_BLOCK);
     need[glq::FP8_WS_S] = std::max(need[glq::FP8_WS_S], (size_t)B * L->KB * sizeof(float));
 }
@@ -124,7 +122,7 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
     const glq_status ok = glq::fp8_workspace(L->device, need, st, buf);
     if (ok != GLQ_OK) return ok;
     int source = 2;
-    if (!q && rounds_inside(B)) source = x_dtype;
+    if (!q && rounds_inside(L, B)) source = x_dtype;
     if (!q && source == 2) {
         glq::Fp8QuantParams p{};
         p.x = x;

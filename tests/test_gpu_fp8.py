@@ -121,6 +121,23 @@ def test_long_batch_in_slices(glq):
     layer.check()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n", [(392, 1160), (16384, 6400)])
+def test_rounding_inside_and_in_front(glq, m, n, dt):
+    """Few tokens, rounded by the product (the smaller layer: up to 8, the larger: up to 4) or before it: the same bits."""
+    gen = torch.Generator().manual_seed(9)
+    layer, _, _ = _layer(glq, gen, m, n)
+    for B in range(1, 11):
+        x = _x(gen, B, n, DT[dt])
+        if B > 2:
+            x[B - 1, 5], x[1, n - 1] = float("nan"), float("inf")
+        y = layer(x.cuda())
+        want = layer.forward_quantized(*glq.fp8_quantize(x.cuda()), out_dtype=DT[dt])
+        assert torch.equal(torch.nan_to_num(y, nan=7.0), torch.nan_to_num(want, nan=7.0))
+        assert torch.equal(torch.isnan(y), torch.isnan(want))
+    layer.check()
+
+
 @pytest.mark.parametrize("B", [1, 16, 17, 100, 400])
 def test_quantized_input_gives_the_same(glq, B):
     gen = torch.Generator().manual_seed(B)
