@@ -21,6 +21,9 @@
 // Warps: 0 copies (TMA of the e4m3 rows and of the laid-out weight tiles, both
 // completing on the first CTA's barrier), 1 MMA (first CTA) and TMEM, 4-11
 // drain.  Every wait is bounded; a timeout sets the layer's error word.
+// Measured: 4096x14336, 2048 rounded tokens 138.5 us = 1.74 PFLOP/s; a K block
+// takes about 1190 cycles, the way round from an accumulator's MMAs to its
+// reuse, and the tensor pipe is busy 45 % of them.
 #include "glq_fp8.cuh"
 #include "glq_kernels.cuh"
 

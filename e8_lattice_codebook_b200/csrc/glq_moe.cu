@@ -12,10 +12,12 @@
 // takes the expert's own tokens as its N side, one behind the other: with all
 // tokens there a stage has to hold 64 of them, and 7 stages instead of 11 kept
 // too few weights in flight (64 tokens of 32 experts of 4096 x 2048: 177 us
-// instead of 148).  The tiles of a phase form
-// one sequence, expert by expert, dealt out evenly over the CTAs, one per SM,
-// so that an odd number of experts or rows leaves no SM idle; a tile that falls
-// to two or more CTAs is summed by whoever reads it, in the order of the CTAs.
+// instead of 148).  The tiles of a phase form one sequence, expert by expert,
+// dealt out evenly over the CTAs, one per SM, so that an odd number of experts
+// or rows leaves no SM idle; a tile that falls to two or more CTAs is summed by
+// whoever reads it, in the order of the CTAs.  One token of 8 of 128 experts of
+// 2048 x 768 takes 23.3 us, of which the weights need 5.8; 16 tokens,
+// 28 experts of 4096 x 2048, 124 us = 5.7 TB/s.
 // Phases, with a barrier over the grid (a cooperative launch) after each:
 //   0  every CTA: the routing of all tokens, for itself; a share of x^
 //   1  gate and up tiles -> fp32 sums per (token, expert)
