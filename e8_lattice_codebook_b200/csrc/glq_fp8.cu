@@ -521,22 +521,22 @@ bool fp8_rounds_inside(int64_t B, int64_t tiles, int KB, int num_sms) {
 
 Fp8SkinnyPlan plan_fp8_skinny(int64_t tiles, int KB, int nt, const int clusters[9]) {
     // A call takes about 2.4 us beside its blocks.  One CTA takes a block in
-    // 0.22 us (16 tokens) to 0.4 us (64) by itself, all together at the HBM's
+    // 0.22 us (16 tokens) to 0.31 us (64) by itself, all together at the HBM's
     // rate (16 KB at 5.9 TB/s: 0.0028 us), and near both bounds the two add up
     // like a norm.  Summing the parts of a split tile costs 1 us at 16 tokens,
     // 2.5 us at 64, and more the larger the cluster.  Measured with C = 1, 2,
     // 3, 4, 6, 8 at one token: 4096x14336 28.8, 17.0, 13.9, 12.6, 15.2, 17.2 us
     // (plan 4); 5120x32768 61, 35, 27.7, 38, 30, 33 us (plan 3); 11008x2048 7.0,
     // 8.3, 10.5, 9.6, 13.1, 16.0 us (plan 1); 1024x8192 17.3, 11.2, 8.8, 7.3, 6.2,
-    // 5.4 us (plan 8).  At 64 tokens: 2560x960 6.6, 7.9, 7.5, 6.8, 7.7, 11.0 us
-    // (plan 1); 4096x4096 16.1, 13.1, 11.8, 10.7, 14.2, 17.3 us (plan 4).
+    // 5.4 us (plan 8).  At 64 tokens: 2560x960 5.8, 7.2, 7.7, 6.9, 7.7, 11.4 us
+    // (plan 1); 4096x4096 14.0, 12.3, 11.3, 10.2, 13.5, 17.0 us (plan 4).
     Fp8SkinnyPlan best{1, (int)(tiles < clusters[1] ? tiles : clusters[1])};
     double best_t = 1e30;
     for (int c = 1; c <= 8 && c <= KB; ++c) {
         if (clusters[c] < 1) continue;
         const int64_t nc = tiles < clusters[c] ? tiles : clusters[c];
         const int64_t rounds = (tiles + nc - 1) / nc;
-        const double alone = (double)(rounds * ((KB + c - 1) / c)) * (0.16 + 0.00375 * nt);
+        const double alone = (double)(rounds * ((KB + c - 1) / c)) * (0.19 + 0.0019 * nt);
         const double hbm = (double)tiles * KB * 0.0028;
         const double t = 2.4 + std::cbrt(alone * alone * alone + hbm * hbm * hbm) +
                          (c > 1 ? 0.4 + nt / 32.0 + 0.1 * c : 0.0);

@@ -217,7 +217,7 @@ struct Pipe {
     static constexpr int TMEM_COLS = NT == 16 ? 256 : 512;
     static_assert(STAGES * NT <= TMEM_COLS, "a slot per stage");
     static constexpr int HALF = NT / 2;     // tokens of one drain set
-    static constexpr int DRAIN = NT <= 32 ? 2 : 1;  // blocks a drain warp takes at once
+    static constexpr int DRAIN = 2;         // blocks a drain warp takes at once
     // Token-operand warps in turn.  A warp's next block is X_TURN after its
     // last, whose begin showed block (last - STAGES) drained; the parity of a
     // barrier tells phases apart only one back, so X_TURN may not exceed the
@@ -348,12 +348,14 @@ __device__ __forceinline__ void pipe_x_done(Pipe<NT> &p, uint32_t it, int lane) 
 
 // A drain warp: adds blocks it .. it + N - 1 to acc (its half of the tokens).
 // The last block's wait covers the others (MMAs complete in order); several
-// blocks share its cost, about 300 cycles for wait, TMEM load and arrive.
+// blocks share its cost, about 300 cycles for wait, TMEM load and arrive (one
+// block at a time, 64 tokens of 32768x5120 took 37.6 us instead of 34.8; three
+// or four keep too many stages waiting: 40.0).
 template <int NT, int N>
 __device__ __forceinline__ bool pipe_drain(Pipe<NT> &p, uint32_t it, int quadrant, int set, float (&acc)[NT / 2],
                                            unsigned *err) {
     constexpr int HALF = NT / 2, STAGES = Pipe<NT>::STAGES;
-    constexpr int STEP = HALF < 32 ? HALF : 32;
+    constexpr int STEP = HALF < 16 ? HALF : 16;
     const uint32_t last = it + N - 1;
     if (!p.wait_warp(&p.done[last % STAGES], (last / STAGES) & 1, err)) return false;
     sm100::tc_fence_after();

@@ -480,11 +480,11 @@ __device__ __forceinline__ void moe_body(const MoeParams &p, const Routing &z, B
 #pragma unroll
                     for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
                     for (uint32_t n = 0; ok && n < len;) {
-                        const bool two = DRAIN == 2 && n + 2 <= len;
+                        const bool two = n + DRAIN <= len;
                         ok = two ? pipe_drain<NT, DRAIN>(pipe, i, quadrant, set, acc, p.err)
                                  : pipe_drain<NT, 1>(pipe, i, quadrant, set, acc, p.err);
-                        n += two ? 2 : 1;
-                        i += two ? 2 : 1;
+                        n += two ? DRAIN : 1;
+                        i += two ? DRAIN : 1;
                     }
                     if (!ok) break;
 #pragma unroll
