@@ -10,14 +10,14 @@
 // Bound by HBM: the weights of every chosen expert are read once, 16 KB tile
 // by tile (glq_fp8.h), by the few-token pipeline of glq_fp8.cuh, whose MMA
 // takes the expert's own tokens as its N side, one behind the other: with all
-// tokens there a stage has to hold 64 of them, and 7 stages instead of 11 kept
-// too few weights in flight (64 tokens of 32 experts of 4096 x 2048: 177 us
-// instead of 148).  The tiles of a phase form one sequence, expert by expert,
-// dealt out evenly over the CTAs, one per SM, so that an odd number of experts
-// or rows leaves no SM idle; a tile that falls to two or more CTAs is summed by
-// whoever reads it, in the order of the CTAs.  One token of 8 of 128 experts of
-// 2048 x 768 takes 23.3 us, of which the weights need 5.8; 16 tokens,
-// 28 experts of 4096 x 2048, 124 us = 5.7 TB/s.
+// tokens there the drain of a block took as long as an SM's share of the HBM
+// (64 tokens of 32 experts of 4096 x 2048: 177 us instead of 148).  The tiles
+// of a phase form one sequence, expert by expert, dealt out evenly over the
+// CTAs, one per SM, so that an odd number of experts or rows leaves no SM idle;
+// a tile that falls to two or more CTAs is summed by whoever reads it, in the
+// order of the CTAs.  One token of 8 of 128 experts of 2048 x 768 takes 23.6 us,
+// of which the weights need 5.8; 16 tokens, 28 experts of 4096 x 2048, 124 us =
+// 5.7 TB/s.
 // Phases, with a barrier over the grid (a cooperative launch) after each:
 //   0  every CTA: the routing of all tokens, for itself; a share of x^
 //   1  gate and up tiles -> fp32 sums per (token, expert)
@@ -583,8 +583,9 @@ constexpr size_t ring_bytes(int max_nt) {
 // through memory go.
 //
 // The body's NT is the smallest that holds the tokens of every expert; 64
-// tokens rarely bring one expert more than 16.  A stage is then 18 KB instead
-// of 24 and there are 11 instead of 7 (179 -> 148 us, as above).
+// tokens rarely bring one expert more than 16.  A block of 16 tokens is drained
+// in half the time of one of 64, two at a time (179 -> 148 us, as above; the
+// number of stages, 8 to 11, makes no difference).
 // LOCAL_T: 4 tokens of 128 experts of 2048 x 768 took 38 us (LOCAL) and 42 us,
 // 8 tokens of 32 experts of 4096 x 2048 111 us and 101 us.
 template <int MAX_NT, bool LOCAL>
