@@ -45,6 +45,7 @@ EXPORTS = (
     "glq_rht_input_operand", "glq_layer_selftest_wait",
     "glq_fp8_quantize", "glq_fp8_create", "glq_fp8_destroy", "glq_fp8_reserve", "glq_fp8_linear",
     "glq_fp8_linear_quantized", "glq_fp8_dequant", "glq_fp8_check", "glq_fp8_info", "glq_fp8_selftest_wait",
+    "glq_fp8_plan",
     "glq_moe_create", "glq_moe_destroy", "glq_moe_reserve", "glq_moe_forward", "glq_moe_check", "glq_moe_info",
 )
 
@@ -107,6 +108,7 @@ _SIGNATURES = {
     "glq_fp8_dequant": ([_vp, _vp, _vp], ctypes.c_int),
     "glq_fp8_check": ([_vp, _vp], ctypes.c_int),
     "glq_fp8_selftest_wait": ([_vp, ctypes.c_int, _i64, _vp], ctypes.c_int),
+    "glq_fp8_plan": ([_vp, _i64] + [ctypes.POINTER(_i32)] * 4 + [ctypes.POINTER(_i64)], ctypes.c_int),
     "glq_fp8_info": ([_vp, ctypes.POINTER(_i64), ctypes.POINTER(_i64), ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
     "glq_moe_create": ([ctypes.POINTER(MoeConfig), _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(_vp)], ctypes.c_int),
     "glq_moe_destroy": ([_vp], ctypes.c_int),
@@ -385,6 +387,13 @@ def glq_fp8_check(handle, stream) -> None:
 
 def glq_fp8_selftest_wait(handle, arrivals, limit, stream) -> None:
     _ok(_L().glq_fp8_selftest_wait(handle, arrivals, limit, stream), "glq_fp8_selftest_wait")
+
+
+def glq_fp8_plan(handle, B) -> dict:
+    kernel, cluster, clusters, ksplit, items = _i32(), _i32(), _i32(), _i32(), _i64()
+    _ok(_L().glq_fp8_plan(handle, B, *(ctypes.byref(v) for v in (kernel, cluster, clusters, ksplit, items))), "glq_fp8_plan")
+    return {"kernel": kernel.value, "cluster": cluster.value, "clusters": clusters.value, "ksplit": ksplit.value,
+            "items": items.value}
 
 
 def glq_fp8_info(handle):
@@ -762,6 +771,9 @@ class Fp8Linear:
         w = torch.empty((self.m, self.n), dtype=torch.float32, device=self.device)
         glq_fp8_dequant(self.handle, w.data_ptr(), _call_stream(self._index, stream, w))
         return w
+
+    def plan(self, B: int) -> dict:
+        return glq_fp8_plan(self.handle, B)
 
     def selftest_wait(self, arrivals: int, limit: int, stream=None):
         """One bounded wait of the kernels on a barrier `arrivals` of its two

@@ -410,6 +410,31 @@ glq_status glq_fp8_selftest_wait(glq_fp8 L, int arrivals, int64_t limit, void *s
                                                   static_cast<cudaStream_t>(stream)));
 }
 
+glq_status glq_fp8_plan(glq_fp8 L, int64_t B, int32_t *kernel, int32_t *cluster, int32_t *clusters, int32_t *ksplit,
+                        int64_t *items) {
+    if (!L) return GLQ_ERR_INVALID_ARG;
+    if (B < 1 || B > MAX_SLICE) return GLQ_ERR_SHAPE;
+    const bool many = B > glq::FP8_FEW;
+    int c = 2, n = 0, ks = 1;
+    int64_t all = L->RT;
+    if (many) {
+        const glq::Fp8GemmParams p = gemm_params(L, B);
+        ks = p.ksplit;
+        all = (int64_t)p.tiles * ks;
+        n = (int)std::min<int64_t>(all, L->num_sms / 2);
+    } else {
+        const glq::Fp8SkinnyPlan plan = glq::plan_fp8_skinny(L->RT, L->KB, glq::fp8_skinny_tile(B), L->clusters);
+        c = plan.C;
+        n = plan.clusters;
+    }
+    if (kernel) *kernel = many ? 1 : 0;
+    if (cluster) *cluster = c;
+    if (clusters) *clusters = n;
+    if (ksplit) *ksplit = ks;
+    if (items) *items = all;
+    return GLQ_OK;
+}
+
 glq_status glq_fp8_info(glq_fp8 L, int64_t *m, int64_t *n, size_t *device_bytes) {
     if (!L) return GLQ_ERR_INVALID_ARG;
     if (m) *m = L->m;

@@ -562,6 +562,17 @@ GLQ_API glq_status glq_fp8_check(glq_fp8 layer, void *stream);
  */
 GLQ_API glq_status glq_fp8_selftest_wait(glq_fp8 layer, int arrivals, int64_t limit, void *stream);
 
+/*
+ * glq_fp8_plan -- measurement / test entry point: how a call of B tokens
+ * (1 <= B <= 8192) runs on this layer.  kernel: 0 the one for few tokens, 1
+ * the GEMM; cluster: CTAs that share a tile; clusters: how many of them are
+ * launched; ksplit: parts of K through the workspace (GEMM); items: tiles
+ * times parts, which the clusters take in turn.  Any output may be NULL.
+ * Errors: GLQ_ERR_INVALID_ARG, GLQ_ERR_SHAPE (B out of range).
+ */
+GLQ_API glq_status glq_fp8_plan(glq_fp8 layer, int64_t B, int32_t *kernel, int32_t *cluster, int32_t *clusters,
+                                int32_t *ksplit, int64_t *items);
+
 /* Layer geometry.  Any output may be NULL. */
 GLQ_API glq_status glq_fp8_info(glq_fp8 layer, int64_t *m, int64_t *n, size_t *device_bytes);
 
