@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
             const int groups = (live + 3) >> 2;
             const int mine = groups > (int)rank ? (groups - (int)rank - 1) / (int)C + 1 : 0;  // this CTA sums
             if (!met) cluster_wait(), met = true;
-            if (!pipe.wait_warp(&pipe.red_empty, (round & 1) ^ 1, p.err)) break;
+            if (!pipe.template wait_warp<true>(&pipe.red_empty, (round & 1) ^ 1, p.err)) break;
             if (dtid == 0) mbar_expect_tx(&pipe.red_full, (uint32_t)(mine * (int)C * width) * (128 * 4));
             if (width == 1) {
                 if (set == 0)
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1) fp8_skinny_kernel(const __gri
                                   remote_smem(&pipe.red_full, to));
                 }
             }
-            if (!pipe.wait_warp(&pipe.red_full, round & 1, p.err)) break;
+            if (!pipe.template wait_warp<true>(&pipe.red_full, round & 1, p.err)) break;
             // a warp sums 32 rows of a group
             for (int u = dtid >> 5; u < mine * 4; u += D_WARPS) {
                 const int own = u >> 2, r = (u & 3) * 32 + lane, row = t * 128 + r;

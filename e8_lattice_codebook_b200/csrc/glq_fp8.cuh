@@ -93,31 +93,44 @@ __device__ __forceinline__ uint32_t round4(uint2 w, float inv) {
 }
 
 // ---------------------------------------------------------------------------
-// Waits: CTA scope, bounded.  (try_wait, with and without a suspend hint, took
-// the same time within 5 %, now more, now less.)
+// Waits, bounded.  CTA scope, or (CLUSTER) cluster scope: for barriers behind
+// which values lie that another CTA of the cluster stored here, or that say
+// that another CTA has read what it was sent; two per tile, not one per block.
+// (try_wait, with and without a suspend hint, took the same time within 5 %,
+// now more, now less.)
 // ---------------------------------------------------------------------------
 
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
     return done != 0;
 }
 
 // false once `limit` cycles have passed, here (then *abort is set and the
 // error word says so) or elsewhere in the CTA
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned *err,
                                              uint64_t limit = WAIT_CYCLES) {
-    if (mbar_test(bar, parity)) return true;
+    if (mbar_test<CLUSTER>(bar, parity)) return true;
     const uint64_t t0 = sm100::clock_cycles();
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
-            if (mbar_test(bar, parity)) return true;
+            if (mbar_test<CLUSTER>(bar, parity)) return true;
         if (*abort) return false;
         if (sm100::clock_cycles() - t0 > limit) {
             atomicOr(err, GLQ_DEVERR_TIMEOUT);
@@ -256,15 +269,17 @@ struct Pipe {
         atomicOr(err, GLQ_DEVERR_TIMEOUT);
         abort = 1;
     }
+    template <bool CLUSTER = false>
     __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, unsigned *err) {
-        return wait_bounded(bar, parity, &abort, err);
+        return wait_bounded<CLUSTER>(bar, parity, &abort, err);
     }
     // The same for a whole warp: one lane waits and __syncwarp orders the
     // others after it.  A poll by all 32 lanes takes the mbarrier unit 32
     // turns: every wait of the CTA then takes hundreds of cycles.
+    template <bool CLUSTER = false>
     __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, unsigned *err) {
         bool ok = true;
-        if ((threadIdx.x & 31) == 0) ok = wait(bar, parity, err);
+        if ((threadIdx.x & 31) == 0) ok = wait<CLUSTER>(bar, parity, err);
         __syncwarp();
         return __shfl_sync(0xffffffffu, ok, 0);
     }

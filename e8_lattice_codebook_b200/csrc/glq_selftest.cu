@@ -30,24 +30,32 @@ __global__ void wait_selftest_kernel(unsigned *err, int kind, int arrivals, unsi
     if (!ok) atomicOr(err, GLQ_DEVERR_TIMEOUT);
 }
 
-// The same for the wait of the 8-bit float kernels.
+// The same for the waits of the 8-bit float kernels, at CTA scope (warp 0)
+// and at cluster scope (warp 1) at once; should only one of them run out,
+// the word says so with GLQ_DEVERR_BOUNDS.
 __global__ void fp8_wait_selftest_kernel(unsigned *err, int arrivals, unsigned long long limit) {
-    __shared__ uint64_t bar;
-    __shared__ volatile int abort;
-    if (threadIdx.x == 0) {
-        mbar_init(&bar, 2);
-        abort = 0;
+    __shared__ uint64_t bar[2];
+    __shared__ volatile int abort[2];
+    __shared__ unsigned ran_out[2];
+    const int t = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+        mbar_init(&bar[t], 2);
+        abort[t] = 0;
+        ran_out[t] = 0;
+        for (int i = 0; i < arrivals; ++i) sm100::mbar_arrive(&bar[t]);
+        if (t == 0) fp8::wait_bounded<false>(&bar[t], 0, &abort[t], &ran_out[t], limit);
+        else fp8::wait_bounded<true>(&bar[t], 0, &abort[t], &ran_out[t], limit);
     }
     __syncthreads();
     if (threadIdx.x != 0) return;
-    for (int i = 0; i < arrivals; ++i) sm100::mbar_arrive(&bar);
-    fp8::wait_bounded(&bar, 0, &abort, err, limit);
+    if (ran_out[0] != ran_out[1]) atomicOr(err, GLQ_DEVERR_BOUNDS);
+    else if (ran_out[0]) atomicOr(err, ran_out[0]);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_wait_selftest(unsigned *err, int arrivals, unsigned long long limit, cudaStream_t s) {
-    fp8_wait_selftest_kernel<<<1, 32, 0, s>>>(err, arrivals, limit);
+    fp8_wait_selftest_kernel<<<1, 64, 0, s>>>(err, arrivals, limit);
     return cudaGetLastError();
 }
 
