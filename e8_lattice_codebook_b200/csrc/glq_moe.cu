@@ -117,7 +117,14 @@ __device__ __forceinline__ void route(const MoeParams &p, int t, int lane, int16
     }
     const float l = key_logit(mine);
     float w = 0.f;
-    if (mine) w = p.scoring == 0 ? expf(l - top) : 1.f / (1.f + expf(-l));
+    if (mine) {
+        if (p.scoring == 0) w = expf(l - top);
+        // The quotient of two scores is a number where the scores vanish in fp32
+        // (logits below -87): relative to the largest, exp(l) = exp(top) exp(l -
+        // top) having its factor in all of them.
+        else if (p.renormalize) w = expf(fminf(l, 0.f) - fminf(top, 0.f)) / (1.f + expf(-fabsf(l)));
+        else w = 1.f / (1.f + expf(-l));
+    }
     if (p.renormalize) sum = warp_sum(w);
     if (p.renormalize || p.scoring == 0) w = w / sum;
     if (lane < p.k) {
