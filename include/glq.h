@@ -589,8 +589,10 @@ GLQ_API glq_status glq_fp8_info(glq_fp8 layer, int64_t *m, int64_t *n, size_t *d
  *     h_e = silu(gate_e x) * (up_e x), y[t] = sum_e p_e down_e h_e,
  * where x and each h_e are rounded as glq_fp8_quantize does and each product
  * is that of an 8-bit float layer.  Sums are fp32, y is rounded once.  A
- * logit of +infinity gives its token NaN.  The order in which a token's sums
- * are added depends on the other tokens of the call.  (No counterpart in the
+ * logit of +infinity gives its token NaN (GLQ_MOE_SOFTMAX) or counts as a
+ * score of 1 (GLQ_MOE_SIGMOID).  Without renormalize a sigmoid below fp32's
+ * range counts 0.  The order in which a token's sums are added depends on
+ * the other tokens of the call.  (No counterpart in the
  * GLQ pages.)
  * ---------------------------------------------------------------------------
  */

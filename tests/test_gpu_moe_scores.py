@@ -55,3 +55,20 @@ def test_renormalized_sigmoid_over_the_range(glq, T):
     logits[0] = torch.finfo(torch.float32).min
     logits[1] = -100.0                        # equal, and far below
     _check(layer(x, logits, out_dtype=torch.float32), x, logits, experts, 4, True, 1, 2.5)
+
+
+def test_infinite_scores(glq):
+    """An infinite logit: its sigmoid is 1, its softmax is none."""
+    gen = torch.Generator("cuda").manual_seed(42)
+    experts = _experts(gen, 6, 136, 136)
+    x = torch.randn(5, 136, generator=gen, device="cuda").to(torch.float16)
+    logits = torch.randn(5, 6, generator=gen, device="cuda")
+    logits[1, 3] = float("inf")
+    as_one = logits.clone()
+    as_one[1, 3] = 1e4                        # sigmoid: exactly 1 in 64 bits
+    for renormalize in (False, True):
+        layer = _layer(glq, experts, 2, renormalize=renormalize, scoring=glq.GLQ_MOE_SIGMOID)
+        y = layer(x, logits, out_dtype=torch.float32)
+        _check(y, x, as_one, experts, 2, renormalize, 1, 1.0)
+        y = _layer(glq, experts, 2, renormalize=renormalize)(x, logits, out_dtype=torch.float32)
+        assert torch.isnan(y[1]).all() and torch.isfinite(y[[0, 2, 3, 4]]).all()
