@@ -1348,17 +1348,7 @@ glq_status glq_layer_selftest_wait(glq_layer L, int kind, int arrivals, int64_t 
 glq_status glq_layer_check(glq_layer L, void *stream) {
     if (!L) return GLQ_ERR_INVALID_ARG;
     DeviceGuard guard(L->device);
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) {
-        cudaGetLastError();
-        return GLQ_ERR_CUDA;
-    }
-    unsigned err = 0;
-    if (cudaMemcpy(&err, L->d_err, sizeof err, cudaMemcpyDeviceToHost) != cudaSuccess) return GLQ_ERR_CUDA;
-    if (err) {
-        cudaMemset(L->d_err, 0, sizeof(unsigned));
-        return (err & GLQ_DEVERR_TIMEOUT) ? GLQ_ERR_TIMEOUT : GLQ_ERR_DEVICE_CHECK;
-    }
-    return GLQ_OK;
+    return glq::take_error(L->d_err, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

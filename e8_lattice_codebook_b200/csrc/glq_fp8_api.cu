@@ -177,18 +177,6 @@ glq_status run_fp8(glq_fp8 L, const void *x, int x_dtype, const uint8_t *q, cons
     return launched(glq::launch_fp8_skinny(p, qmap, source, nt, plan.clusters, st, true));
 }
 
-glq_status check_word(unsigned *d_err, cudaStream_t s) {
-    if (cudaStreamSynchronize(s) != cudaSuccess) {
-        cudaGetLastError();
-        return GLQ_ERR_CUDA;
-    }
-    unsigned err = 0;
-    if (cudaMemcpy(&err, d_err, sizeof err, cudaMemcpyDeviceToHost) != cudaSuccess) return GLQ_ERR_CUDA;
-    if (!err) return GLQ_OK;
-    cudaMemset(d_err, 0, sizeof(unsigned));
-    return (err & GLQ_DEVERR_TIMEOUT) ? GLQ_ERR_TIMEOUT : GLQ_ERR_DEVICE_CHECK;
-}
-
 // ---------------------------------------------------------------------------
 // Mixture of experts
 // ---------------------------------------------------------------------------
@@ -400,7 +388,7 @@ glq_status glq_fp8_dequant(glq_fp8 L, float *w_dev, void *stream) {
 glq_status glq_fp8_check(glq_fp8 L, void *stream) {
     if (!L) return GLQ_ERR_INVALID_ARG;
     DeviceGuard guard(L->device);
-    return check_word(L->d_err, static_cast<cudaStream_t>(stream));
+    return glq::take_error(L->d_err, static_cast<cudaStream_t>(stream));
 }
 
 glq_status glq_fp8_selftest_wait(glq_fp8 L, int arrivals, int64_t limit, void *stream) {
@@ -582,10 +570,8 @@ glq_status glq_moe_forward(glq_moe L, const void *x_dev, glq_dtype x_dtype, cons
 glq_status glq_moe_check(glq_moe L, void *stream) {
     if (!L) return GLQ_ERR_INVALID_ARG;
     DeviceGuard guard(L->device);
-    const glq_status st = check_word(L->d_err, static_cast<cudaStream_t>(stream));
     // a call that gave up may have left the grid barrier half way
-    if (st == GLQ_ERR_TIMEOUT) cudaMemset(L->d_bar, 0, sizeof(uint64_t));
-    return st;
+    return glq::take_error(L->d_err, static_cast<cudaStream_t>(stream), L->d_bar);
 }
 
 glq_status glq_moe_info(glq_moe L, glq_moe_config *config, size_t *device_bytes) {

@@ -144,6 +144,29 @@ struct DeviceGuard {
     }
 };
 
+// Waits for `s`, reads a layer's error word and, if it says something, clears it
+// and after a timeout also `after_timeout` (may be null).  All on `s`, and
+// waited for: the legacy stream is not ordered with a call that follows on a
+// non-blocking one, whose arrivals or errors a late clear would wipe out.
+inline glq_status take_error(unsigned *d_err, cudaStream_t s, uint64_t *after_timeout = nullptr) {
+    unsigned err = 0;
+    bool ok = cudaStreamSynchronize(s) == cudaSuccess &&
+              cudaMemcpyAsync(&err, d_err, sizeof err, cudaMemcpyDeviceToHost, s) == cudaSuccess &&
+              cudaStreamSynchronize(s) == cudaSuccess;
+    if (ok && err) {
+        ok = cudaMemsetAsync(d_err, 0, sizeof err, s) == cudaSuccess;
+        if (ok && after_timeout && (err & GLQ_DEVERR_TIMEOUT))
+            ok = cudaMemsetAsync(after_timeout, 0, sizeof *after_timeout, s) == cudaSuccess;
+        ok = ok && cudaStreamSynchronize(s) == cudaSuccess;
+    }
+    if (!ok) {
+        cudaGetLastError();
+        return GLQ_ERR_CUDA;
+    }
+    if (!err) return GLQ_OK;
+    return (err & GLQ_DEVERR_TIMEOUT) ? GLQ_ERR_TIMEOUT : GLQ_ERR_DEVICE_CHECK;
+}
+
 // The 8-bit float operators' buffers in the device's shared workspace:
 // rounded activations, their scales, parts of a split K, all of a mixture-of-
 // experts call.
