@@ -836,6 +836,7 @@ glq_status glq_codebook_upload(const uint16_t *host_fp16_bits, int32_t entries, 
                                        cudaMemcpyHostToDevice) != cudaSuccess)
             st = GLQ_ERR_CUDA;
     }
+    if (st == GLQ_OK && cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) st = GLQ_ERR_CUDA;
     if (st != GLQ_OK) {
         cudaFree(cb->d_fp16);
         cudaFree(cb->d_table);
@@ -983,6 +984,9 @@ static glq_status create_layer(int64_t m, int64_t n, int32_t bpw, const uint16_t
         ok = ok && cudaMemset(L->d_err, 0, sizeof(unsigned)) == cudaSuccess;
         ok = ok && cudaMemset(L->d_cnt, 0, (size_t)max_bands * sizeof(unsigned)) == cudaSuccess;
         ok = ok && cudaMemset(L->d_blk_cnt, 0, GLQ_MAX_BLOCKS * sizeof(unsigned)) == cudaSuccess;
+        // the clears, and a copy's last step, may still be under way: a call may
+        // follow on a stream that does not wait for this one
+        ok = ok && cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess;
         if (!ok) st = GLQ_ERR_CUDA;
     }
     if (st != GLQ_OK) {

@@ -1,10 +1,12 @@
 """Reading and clearing a layer's error word happens on the stream that check()
-is given, and is over when it returns."""
+is given, and is over when it returns; so is the making of a layer."""
+import numpy as np
 import pytest
 
 import fp8_device_reference as ref
 import glq_inputs as gi
-from gpu_helpers import Device
+from gpu_helpers import Device, to_torch_x, tolerance
+from oracle import glq_oracle as orc
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +52,19 @@ def test_check_uses_its_stream_alone(glq):
         assert outcomes == [9, 0, 9, 0]
         assert still_busy  # nothing of a check waited for, or was put behind, the default stream's work
         layer.check()
+
+
+def test_layer_is_made_when_the_call_returns(glq):
+    """A call on a stream that waits for no other, straight after the layer was made."""
+    L = gi.make_layer(52, 0, 1024, 1024, 3)
+    xb = gi.make_x(52, 0, 4, L.n, "bf16")
+    x, y = to_torch_x(xb, "bf16"), torch.empty(4, L.m, device="cuda")
+    ref_y = orc.linear(L.m, L.n, L.bpw, L.idx1, L.idx2, L.weight_scale, L.resid_scale, L.s_in, L.s_out, xb, True,
+                       cb2=L.cb2_f16)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        layer = Device().layer(L)
+        layer(x, out=y, stream=side)
+        layer.check(stream=side)
+        assert np.max(np.abs(y.cpu().numpy().astype(np.float64) - ref_y)) <= tolerance(ref_y)
