@@ -631,6 +631,21 @@ def _call_stream(index, stream, *tensors):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A call's result, allocated on the stream that will write it: a block of
+    the current stream's could still be read by work queued there, which a
+    call on another stream does not wait for.  The current stream is recorded
+    as a reader, so that the block stays while that has work with it."""
+    torch = _torch()
+    current = torch.cuda.current_stream(device)
+    if stream is None or stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
+
+
 def _fp8_dtypes():
     global _E4M3_F32
     if _E4M3_F32 is None:
@@ -692,11 +707,12 @@ def fp8_quantize(x, q=None, s=None, stream=None):
     e4m3, f32 = _fp8_dtypes()
     G = _fp8_blocks(n)
     if q is None:
-        q = x.new_empty((B, G * FP8_BLOCK), dtype=e4m3)
+        shape = (B, G * FP8_BLOCK)
+        q = x.new_empty(shape, dtype=e4m3) if stream is None else _empty(shape, e4m3, x.device, stream)
     else:
         _check_output("q", q, (B, G * FP8_BLOCK), index)
     if s is None:
-        s = x.new_empty((G, B), dtype=f32)
+        s = x.new_empty((G, B), dtype=f32) if stream is None else _empty((G, B), f32, x.device, stream)
     else:
         _check_output("s", s, (G, B), index)
     if q.dtype != e4m3 or s.dtype != f32:
@@ -736,7 +752,9 @@ class Fp8Linear:
         _check_input("x", x, self.n, self._index)
         B = x.size(0)
         if out is None:
-            out = x.new_empty((B, self.m), dtype=out_dtype)
+            shape = (B, self.m)
+            out = (x.new_empty(shape, dtype=out_dtype) if stream is None
+                   else _empty(shape, out_dtype or x.dtype, x.device, stream))
         else:
             _check_output("out", out, (B, self.m), self._index)
         glq_fp8_linear(self.handle, x.data_ptr(), _dtype_code(x), out.data_ptr(), _dtype_code(out), B,
@@ -758,7 +776,8 @@ class Fp8Linear:
         if s.dtype != torch.float32:
             raise ValueError("s must be float32")
         if out is None:
-            out = s.new_empty((B, self.m), dtype=out_dtype or torch.bfloat16)
+            shape, dtype = (B, self.m), out_dtype or torch.bfloat16
+            out = s.new_empty(shape, dtype=dtype) if stream is None else _empty(shape, dtype, s.device, stream)
         else:
             _check_output("out", out, (B, self.m), self._index)
         glq_fp8_linear_quantized(self.handle, q.data_ptr(), s.data_ptr(), out.data_ptr(), _dtype_code(out), B,
@@ -768,7 +787,7 @@ class Fp8Linear:
     def dequant(self, stream=None):
         """The weights as fp32 [m][n]."""
         torch = _torch()
-        w = torch.empty((self.m, self.n), dtype=torch.float32, device=self.device)
+        w = _empty((self.m, self.n), torch.float32, self.device, stream)
         glq_fp8_dequant(self.handle, w.data_ptr(), _call_stream(self._index, stream, w))
         return w
 
@@ -838,7 +857,9 @@ class Fp8Moe:
         if logits.size(0) != T:
             raise ValueError(f"logits must have {T} rows, as x has")
         if out is None:
-            out = x.new_empty((T, self.d), dtype=out_dtype)
+            shape = (T, self.d)
+            out = (x.new_empty(shape, dtype=out_dtype) if stream is None
+                   else _empty(shape, out_dtype or x.dtype, x.device, stream))
         else:
             _check_output("out", out, (T, self.d), self._index)
         glq_moe_forward(self.handle, x.data_ptr(), _dtype_code(x), logits.data_ptr(), _dtype_code(logits),

@@ -1,0 +1,75 @@
+"""Results that a call on a given stream allocates: they take no block that the
+current stream still reads, and theirs is not taken while it reads them."""
+import pytest
+
+import fp8_device_reference as ref
+import glq_inputs as gi
+from gpu_helpers import Device
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+SLEEP = 100_000_000  # cycles, about 50 ms
+
+
+@pytest.fixture(scope="module")
+def glq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import e8_lattice_codebook_b200 as glq
+    return glq
+
+
+def _calls(glq):
+    gen = torch.Generator("cuda").manual_seed(61)
+    x = torch.randn(24, 264, generator=gen, device="cuda").to(torch.bfloat16)
+    linear = glq.Fp8Linear(*ref.random_weight(gen, 264, 264))
+    experts = []
+    for m, n in ((136, 264), (136, 264), (264, 136)):
+        made = [ref.random_weight(gen, m, n) for _ in range(4)]
+        experts += [torch.stack([w.view(torch.uint8) for w, _ in made]).view(torch.float8_e4m3fn),
+                    torch.stack([s for _, s in made])]
+    moe = glq.Fp8Moe(*experts, topk=2)
+    logits = torch.randn(24, 4, generator=gen, device="cuda")
+    q, s = glq.fp8_quantize(x)
+    return {
+        "quantize": lambda st: glq.fp8_quantize(x, stream=st)[0].view(torch.uint8),
+        "linear": lambda st: linear(x, stream=st),
+        "quantized": lambda st: linear.forward_quantized(q, s, stream=st),
+        "dequant": lambda st: linear.dequant(stream=st),
+        "moe": lambda st: moe(x, logits, stream=st),
+    }
+
+
+def _check(call):
+    want = call(None).clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert torch.equal(call(side), want)  # loads what it needs
+    torch.cuda.synchronize()
+    for _ in range(3):
+        # a block that the current stream has yet to read, given back to the allocator
+        block = torch.full_like(want, 3)
+        torch.cuda._sleep(SLEEP)
+        kept = block.clone()
+        where = block.data_ptr()
+        del block
+        got = call(side)
+        assert got.data_ptr() != where
+        side.synchronize()
+        # a result that the current stream reads late, given back while it has not
+        torch.cuda._sleep(SLEEP)
+        late = got.clone()
+        where = got.data_ptr()
+        del got
+        again = call(side)
+        assert again.data_ptr() != where
+        torch.cuda.synchronize()
+        assert torch.equal(again, want) and torch.equal(late, want)
+        assert torch.equal(kept, torch.full_like(want, 3))
+
+
+@pytest.mark.parametrize("name", ["quantize", "linear", "quantized", "dequant", "moe"])
+def test_fp8_results(glq, name):
+    _check(_calls(glq)[name])

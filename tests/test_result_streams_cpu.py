@@ -1,0 +1,115 @@
+"""Where the binding allocates a call's result when it is given a stream: on
+that stream, whose kernel writes it, with the current stream recorded as a
+reader.  With fakes of torch's allocator and streams, without a GPU."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+import e8_lattice_codebook_b200 as glq
+
+
+class Stream:
+    def __init__(self, raw):
+        self.cuda_stream = raw
+
+
+class World:
+    """The current stream, and tensors that know where they were allocated."""
+
+    def __init__(self):
+        self.main, self.side = Stream(1), Stream(2)
+        self.now = self.main
+        self.launches = []
+        world = self
+
+        class Tensor:
+            is_cuda, device = True, torch.device("cuda", 0)
+
+            def __init__(self, shape, dtype, on):
+                self.shape, self.dtype, self.on, self.recorded = tuple(shape), dtype, on, []
+
+            dim = lambda t: len(t.shape)  # noqa: E731
+            size = lambda t, i: t.shape[i]  # noqa: E731
+            is_contiguous = lambda t: True  # noqa: E731
+            get_device = lambda t: 0  # noqa: E731
+            data_ptr = lambda t: 1 << 20  # noqa: E731
+            record_stream = lambda t, s: t.recorded.append(s)  # noqa: E731
+
+            def new_empty(t, shape, dtype=None):
+                return Tensor(shape, dtype or t.dtype, world.now)
+
+            def __getitem__(t, at):
+                return t
+
+        @contextlib.contextmanager
+        def stream(s):
+            before, world.now = world.now, s
+            yield
+            world.now = before
+
+        self.Tensor = Tensor
+        cuda = types.SimpleNamespace(current_stream=lambda d=None: world.now, stream=stream,
+                                     device=lambda i: contextlib.nullcontext())
+        self.torch = types.SimpleNamespace(
+            cuda=cuda, float16=torch.float16, bfloat16=torch.bfloat16, float32=torch.float32, float8_e4m3fn=torch.float8_e4m3fn,
+            empty=lambda shape, dtype, device: Tensor(shape, dtype, world.now), _C=types.SimpleNamespace(_cuda_getDevice=lambda: 0))
+
+    def layer(self, cls, **fields):
+        layer = cls.__new__(cls)
+        layer.__dict__.update(handle=0, _index=0, device=torch.device("cuda", 0), **fields)
+        return layer
+
+
+@pytest.fixture
+def world(monkeypatch):
+    w = World()
+    monkeypatch.setattr(glq, "_torch", lambda: w.torch)
+    monkeypatch.setattr(glq, "_raw_stream", lambda i: w.now.cuda_stream)
+    monkeypatch.setattr(glq, "_E4M3_F32", None)
+    monkeypatch.setattr(glq, "_DTYPE_CODES", {})
+    for name in ("glq_fp8_quantize", "glq_fp8_linear", "glq_fp8_linear_quantized", "glq_fp8_dequant", "glq_moe_forward"):
+        monkeypatch.setattr(glq, name, lambda *a: w.launches.append(a[-1]))
+    return w
+
+
+def _fp8_calls(w):
+    bf16, x = torch.bfloat16, w.Tensor((5, 264), torch.bfloat16, w.main)
+    linear = w.layer(glq.Fp8Linear, m=136, n=264)
+    moe = w.layer(glq.Fp8Moe, d=264, inter=136, experts=4, topk=2)
+    q, s = w.Tensor((5, 384), torch.float8_e4m3fn, w.main), w.Tensor((3, 5), torch.float32, w.main)
+    logits = w.Tensor((5, 4), torch.float32, w.main)
+    return {
+        "quantize": (lambda st: glq.fp8_quantize(x, stream=st), [x], [torch.float8_e4m3fn, torch.float32]),
+        "linear": (lambda st: linear(x, stream=st), [x], [bf16]),
+        "linear, f32": (lambda st: linear(x, out_dtype=torch.float32, stream=st), [x], [torch.float32]),
+        "quantized": (lambda st: linear.forward_quantized(q, s, stream=st), [q, s], [bf16]),
+        "dequant": (lambda st: linear.dequant(stream=st), [], [torch.float32]),
+        "moe": (lambda st: moe(x, logits, stream=st), [x, logits], [bf16]),
+    }
+
+
+CALLS = ["quantize", "linear", "linear, f32", "quantized", "dequant", "moe"]
+
+
+def _check(w, calls, name):
+    run, inputs, dtypes = calls[name]
+    for given, other in ((w.side, True), (w.main, False), (None, False)):
+        for t in inputs:
+            t.recorded.clear()
+        w.launches.clear()
+        outs = run(given)
+        outs = outs if isinstance(outs, tuple) else (outs,)
+        assert [o.dtype for o in outs] == dtypes
+        assert w.launches == [(given or w.main).cuda_stream]
+        for o in outs:
+            assert o.on is (given or w.main), name
+            assert (w.main in o.recorded) == other
+        for t in inputs:
+            assert (w.side in t.recorded) == other
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_fp8_results(world, name):
+    _check(world, _fp8_calls(world), name)
