@@ -461,6 +461,30 @@ def _stream_ptr(stream):
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A call's result, allocated on the stream that will write it: a block of
+    the current stream's could still be read by work queued there, which a
+    call on another stream does not wait for.  The current stream is recorded
+    as a reader, so that the block stays while that has work with it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
+
+
+def _used_on(stream, *tensors):
+    """Tensors that a call on `stream` reads or writes stay while it does."""
+    if stream is not None and stream.cuda_stream != _torch().cuda.current_stream(tensors[0].device).cuda_stream:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 class Codebook:
     """A device codebook (65,536 x 8 E8 or 256 x 8 residual), fp16 bits on the host."""
 
@@ -513,7 +537,8 @@ class GlqLinear:
         B = x.shape[0]
         odt = out_dtype or x.dtype
         if out is None:
-            out = torch.empty((B, self.m), dtype=odt, device=x.device)
+            out = _empty((B, self.m), odt, x.device, stream)
+        _used_on(stream, x, out)
         glq_linear(self.handle, x.data_ptr(), dtype_code(x.dtype), out.data_ptr(),
                    dtype_code(out.dtype), B, _stream_ptr(stream))
         return out
@@ -522,13 +547,14 @@ class GlqLinear:
 
     def dequant(self, stream=None):
         torch = _torch()
-        w = torch.empty((self.m, self.n), dtype=torch.float32, device="cuda")
+        w = _empty((self.m, self.n), torch.float32, torch.device("cuda", torch.cuda.current_device()), stream)
         glq_dequant_reference(self.handle, w.data_ptr(), _stream_ptr(stream))
         return w
 
     def rht_input(self, x, stream=None):
         torch = _torch()
-        xr = torch.empty((x.shape[0], self.n), dtype=torch.float32, device=x.device)
+        xr = _empty((x.shape[0], self.n), torch.float32, x.device, stream)
+        _used_on(stream, x)
         glq_rht_input(self.handle, x.data_ptr(), dtype_code(x.dtype), xr.data_ptr(), x.shape[0],
                       _stream_ptr(stream))
         return xr
@@ -540,8 +566,9 @@ class GlqLinear:
         tensor-core path's input stage with the chosen kernel."""
         torch = _torch()
         n_pad = (self.n + 127) // 128 * 128
-        xh = torch.empty((x.shape[0], n_pad), dtype=torch.float16, device=x.device)
-        info = torch.empty((x.shape[0], 4), dtype=torch.float32, device=x.device)
+        xh = _empty((x.shape[0], n_pad), torch.float16, x.device, stream)
+        info = _empty((x.shape[0], 4), torch.float32, x.device, stream)
+        _used_on(stream, x)
         glq_rht_input_operand(self.handle, x.data_ptr(), dtype_code(x.dtype), xh.data_ptr(), info.data_ptr(),
                               x.shape[0], kernel, _stream_ptr(stream))
         return xh, info[:, 2]
@@ -554,7 +581,8 @@ class GlqLinear:
 
     def rht_output(self, z, out_dtype=None, stream=None):
         torch = _torch()
-        y = torch.empty((z.shape[0], self.m), dtype=out_dtype or torch.float32, device=z.device)
+        y = _empty((z.shape[0], self.m), out_dtype or torch.float32, z.device, stream)
+        _used_on(stream, z)
         glq_rht_output(self.handle, z.data_ptr(), y.data_ptr(), dtype_code(y.dtype), z.shape[0],
                        _stream_ptr(stream))
         return y
@@ -629,21 +657,6 @@ def _call_stream(index, stream, *tensors):
     for t in tensors:
         t.record_stream(stream)
     return stream.cuda_stream
-
-
-def _empty(shape, dtype, device, stream):
-    """A call's result, allocated on the stream that will write it: a block of
-    the current stream's could still be read by work queued there, which a
-    call on another stream does not wait for.  The current stream is recorded
-    as a reader, so that the block stays while that has work with it."""
-    torch = _torch()
-    current = torch.cuda.current_stream(device)
-    if stream is None or stream.cuda_stream == current.cuda_stream:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        out = torch.empty(shape, dtype=dtype, device=device)
-    out.record_stream(current)
-    return out
 
 
 def _fp8_dtypes():

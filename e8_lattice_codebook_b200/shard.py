@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import _stream_ptr, dtype_code, glq_cast, glq_layer_create_shard, glq_layer_destroy, glq_linear
+from . import _empty, _stream_ptr, _used_on, dtype_code, glq_cast, glq_layer_create_shard, glq_layer_destroy, glq_linear
 
 CHUNK = 128
 
@@ -50,7 +50,8 @@ class RowParallelLinear:
     def partial(self, x, out=None, stream=None):
         """This rank's fp32 part of y (before the all-reduce)."""
         import torch
-        y = out if out is not None else torch.empty((x.shape[0], self.m), dtype=torch.float32, device=x.device)
+        y = out if out is not None else _empty((x.shape[0], self.m), torch.float32, x.device, stream)
+        _used_on(stream, x, y)
         glq_linear(self.handle, x.data_ptr(), dtype_code(x.dtype), y.data_ptr(), dtype_code(torch.float32),
                    x.shape[0], _stream_ptr(stream))
         return y

@@ -73,3 +73,13 @@ def _check(call):
 @pytest.mark.parametrize("name", ["quantize", "linear", "quantized", "dequant", "moe"])
 def test_fp8_results(glq, name):
     _check(_calls(glq)[name])
+
+
+def test_lattice_results(glq):
+    L = gi.make_layer(62, 0, 264, 256, 3)
+    layer = Device().layer(L)
+    x = torch.randn(24, 256, generator=torch.Generator("cuda").manual_seed(62), device="cuda").to(torch.bfloat16)
+    _check(lambda st: layer(x, stream=st))
+    _check(lambda st: layer(x[:2], out_dtype=torch.float32, stream=st))
+    _check(lambda st: layer.dequant(stream=st))
+    _check(lambda st: layer.rht_input(x, stream=st))

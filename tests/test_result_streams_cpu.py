@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import e8_lattice_codebook_b200 as glq
+from e8_lattice_codebook_b200 import shard
 
 
 class Stream:
@@ -50,10 +51,10 @@ class World:
             world.now = before
 
         self.Tensor = Tensor
-        cuda = types.SimpleNamespace(current_stream=lambda d=None: world.now, stream=stream,
+        cuda = types.SimpleNamespace(current_device=lambda: 0, current_stream=lambda d=None: world.now, stream=stream,
                                      device=lambda i: contextlib.nullcontext())
         self.torch = types.SimpleNamespace(
-            cuda=cuda, float16=torch.float16, bfloat16=torch.bfloat16, float32=torch.float32, float8_e4m3fn=torch.float8_e4m3fn,
+            cuda=cuda, float16=torch.float16, bfloat16=torch.bfloat16, device=torch.device, float32=torch.float32, float8_e4m3fn=torch.float8_e4m3fn,
             empty=lambda shape, dtype, device: Tensor(shape, dtype, world.now), _C=types.SimpleNamespace(_cuda_getDevice=lambda: 0))
 
     def layer(self, cls, **fields):
@@ -69,6 +70,9 @@ def world(monkeypatch):
     monkeypatch.setattr(glq, "_raw_stream", lambda i: w.now.cuda_stream)
     monkeypatch.setattr(glq, "_E4M3_F32", None)
     monkeypatch.setattr(glq, "_DTYPE_CODES", {})
+    for name in ("glq_linear", "glq_dequant_reference", "glq_rht_input", "glq_rht_input_operand", "glq_rht_output"):
+        monkeypatch.setattr(glq, name, lambda *a: w.launches.append(a[-1]))
+    monkeypatch.setattr(shard, "glq_linear", lambda *a: w.launches.append(a[-1]))
     for name in ("glq_fp8_quantize", "glq_fp8_linear", "glq_fp8_linear_quantized", "glq_fp8_dequant", "glq_moe_forward"):
         monkeypatch.setattr(glq, name, lambda *a: w.launches.append(a[-1]))
     return w
@@ -113,3 +117,22 @@ def _check(w, calls, name):
 @pytest.mark.parametrize("name", CALLS)
 def test_fp8_results(world, name):
     _check(world, _fp8_calls(world), name)
+
+
+def _lattice_calls(w):
+    bf16, f32, x = torch.bfloat16, torch.float32, w.Tensor((5, 264), torch.bfloat16, w.main)
+    layer = w.layer(glq.GlqLinear, m=136, n=264)
+    part = w.layer(shard.RowParallelLinear, m=136, n=264)
+    return {
+        "lattice": (lambda st: layer(x, stream=st), [x], [bf16]),
+        "lattice dequant": (lambda st: layer.dequant(stream=st), [], [f32]),
+        "rht in": (lambda st: layer.rht_input(x, stream=st), [x], [f32]),
+        "rht operand": (lambda st: layer.rht_input_operand(x, stream=st), [x], [torch.float16, f32]),
+        "rht out": (lambda st: layer.rht_output(x, stream=st), [x], [f32]),
+        "part": (lambda st: part.partial(x, stream=st), [x], [f32]),
+    }
+
+
+@pytest.mark.parametrize("name", ["lattice", "lattice dequant", "rht in", "rht operand", "rht out", "part"])
+def test_lattice_results(world, name):
+    _check(world, _lattice_calls(world), name)
