@@ -13,7 +13,8 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import _empty, _stream_ptr, _used_on, dtype_code, glq_cast, glq_layer_create_shard, glq_layer_destroy, glq_linear
+from . import _empty, _stream_ptr, _torch, _used_on, dtype_code, glq_cast, glq_layer_create_shard, \
+    glq_layer_destroy, glq_linear
 
 CHUNK = 128
 
@@ -49,7 +50,7 @@ class RowParallelLinear:
 
     def partial(self, x, out=None, stream=None):
         """This rank's fp32 part of y (before the all-reduce)."""
-        import torch
+        torch = _torch()
         y = out if out is not None else _empty((x.shape[0], self.m), torch.float32, x.device, stream)
         _used_on(stream, x, y)
         glq_linear(self.handle, x.data_ptr(), dtype_code(x.dtype), y.data_ptr(), dtype_code(torch.float32),
@@ -58,16 +59,25 @@ class RowParallelLinear:
 
     def __call__(self, x, out_dtype=None, stream=None):
         """y of the whole layer on every rank: partial, all-reduce, cast."""
-        import torch
         import torch.distributed as dist
-        y32 = self.partial(x, stream=stream)
+        torch = _torch()
+        if stream is not None:
+            # the collective waits for the current stream and is waited for there
+            current = torch.cuda.current_stream(x.device)
+            with torch.cuda.stream(stream):
+                y = self(x, out_dtype)
+            if stream.cuda_stream != current.cuda_stream:
+                x.record_stream(stream)
+                y.record_stream(current)
+            return y
+        y32 = self.partial(x)
         if self.world > 1:
             dist.all_reduce(y32, op=dist.ReduceOp.SUM, group=self.group)
         odt = out_dtype or x.dtype
         if odt == torch.float32:
             return y32
         y = torch.empty(y32.shape, dtype=odt, device=y32.device)
-        glq_cast(y32.data_ptr(), y.data_ptr(), dtype_code(odt), y32.numel(), _stream_ptr(stream))
+        glq_cast(y32.data_ptr(), y.data_ptr(), dtype_code(odt), y32.numel(), _stream_ptr(None))
         return y
 
     def close(self):

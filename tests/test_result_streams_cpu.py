@@ -41,6 +41,9 @@ class World:
             def new_empty(t, shape, dtype=None):
                 return Tensor(shape, dtype or t.dtype, world.now)
 
+            def numel(t):
+                return t.shape[0] * t.shape[1]
+
             def __getitem__(t, at):
                 return t
 
@@ -67,6 +70,7 @@ class World:
 def world(monkeypatch):
     w = World()
     monkeypatch.setattr(glq, "_torch", lambda: w.torch)
+    monkeypatch.setattr(shard, "_torch", lambda: w.torch, raising=False)
     monkeypatch.setattr(glq, "_raw_stream", lambda i: w.now.cuda_stream)
     monkeypatch.setattr(glq, "_E4M3_F32", None)
     monkeypatch.setattr(glq, "_DTYPE_CODES", {})
@@ -136,3 +140,21 @@ def _lattice_calls(w):
 @pytest.mark.parametrize("name", ["lattice", "lattice dequant", "rht in", "rht operand", "rht out", "part"])
 def test_lattice_results(world, name):
     _check(world, _lattice_calls(world), name)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_collective_is_on_the_given_stream(world, monkeypatch, dtype):
+    """A shard's sum over the ranks follows the part on its stream, and the rounding follows the sum."""
+    monkeypatch.setattr(torch.distributed, "all_reduce", lambda t, **k: world.launches.append(world.now.cuda_stream))
+    monkeypatch.setattr(shard, "glq_cast", lambda *a: world.launches.append(a[-1]))
+    x = world.Tensor((5, 264), torch.bfloat16, world.main)
+    layer = world.layer(shard.RowParallelLinear, m=136, n=264, rank=0, world=2, group=None)
+    steps = 2 + (dtype != torch.float32)
+    for given in (world.side, world.main, None):
+        world.launches.clear()
+        y = layer(x, out_dtype=dtype, stream=given)
+        assert world.launches == [(given or world.main).cuda_stream] * steps
+        assert y.on is (given or world.main) and y.dtype == dtype
+        assert (world.main in y.recorded) == (given is world.side) == (world.side in x.recorded)
+        x.recorded.clear()
+        assert world.now is world.main
