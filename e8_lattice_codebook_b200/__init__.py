@@ -47,6 +47,7 @@ EXPORTS = (
     "glq_fp8_linear_quantized", "glq_fp8_dequant", "glq_fp8_check", "glq_fp8_info", "glq_fp8_selftest_wait",
     "glq_fp8_plan",
     "glq_moe_create", "glq_moe_destroy", "glq_moe_reserve", "glq_moe_forward", "glq_moe_check", "glq_moe_info",
+    "glq_moe_selftest_wait",
 )
 
 
@@ -115,6 +116,7 @@ _SIGNATURES = {
     "glq_moe_reserve": ([_vp, _i64], ctypes.c_int),
     "glq_moe_forward": ([_vp, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, ctypes.c_int, _i64, _vp], ctypes.c_int),
     "glq_moe_check": ([_vp, _vp], ctypes.c_int),
+    "glq_moe_selftest_wait": ([_vp, ctypes.c_int, _i64, _vp], ctypes.c_int),
     "glq_moe_info": ([_vp, ctypes.POINTER(MoeConfig), ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
 }
 
@@ -427,6 +429,10 @@ def glq_moe_forward(handle, x_ptr, x_dtype, logits_ptr, logits_dtype, y_ptr, y_d
 
 def glq_moe_check(handle, stream) -> None:
     _ok(_L().glq_moe_check(handle, stream), "glq_moe_check")
+
+
+def glq_moe_selftest_wait(handle, arrivals, limit, stream) -> None:
+    _ok(_L().glq_moe_selftest_wait(handle, arrivals, limit, stream), "glq_moe_selftest_wait")
 
 
 def glq_moe_info(handle):
@@ -880,6 +886,12 @@ class Fp8Moe:
         return out
 
     __call__ = forward
+
+    def selftest_wait(self, arrivals: int, limit: int, stream=None):
+        """One bounded wait on the barrier between the kernel's CTAs, of which
+        one (arrivals 1) or none (2) is missing; the outcome reads back through
+        check(), which has to come before the next call."""
+        glq_moe_selftest_wait(self.handle, arrivals, limit, _call_stream(self._index, stream))
 
     def check(self, stream=None):
         glq_moe_check(self.handle, _call_stream(self._index, stream))

@@ -140,6 +140,37 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, vol
     }
 }
 
+__device__ __forceinline__ uint64_t atom_add_u64(uint64_t *p, uint64_t v) {
+    uint64_t old;
+    asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(old) : "l"(p), "l"(v) : "memory");
+    return old;
+}
+__device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t *p) {
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+// One thread of each of the G CTAs of a cooperative launch: the grid's barrier.
+// `bar` counts arrivals over all calls, each of which adds a multiple of G.
+// The same bound and outcome as wait_bounded; after a wait that ran out the
+// counter is no multiple of G until it is cleared.
+__device__ __forceinline__ bool grid_barrier(uint64_t *bar, uint32_t G, volatile int *abort, unsigned *err,
+                                             uint64_t limit = WAIT_CYCLES) {
+    // release: what this CTA's warps wrote before they arrived at this thread
+    const uint64_t old = atom_add_u64(bar, 1);
+    const uint64_t target = (old / G + 1) * G;
+    const uint64_t t0 = sm100::clock_cycles();
+    while (ld_acquire_u64(bar) < target) {
+        if (*abort) return false;
+        if (sm100::clock_cycles() - t0 > limit) {
+            atomicOr(err, GLQ_DEVERR_TIMEOUT);
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // ---------------------------------------------------------------------------
 // tcgen05.mma kind::f8f6f4, e4m3 x e4m3 -> fp32, K = 32 per instruction
 // ---------------------------------------------------------------------------
@@ -264,10 +295,6 @@ struct Pipe {
             mbar_init(&red_empty, ctas * D_WARPS);
             abort = 0;
         }
-    }
-    __device__ __forceinline__ void fail(unsigned *err) {
-        atomicOr(err, GLQ_DEVERR_TIMEOUT);
-        abort = 1;
     }
     template <bool CLUSTER = false>
     __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, unsigned *err) {

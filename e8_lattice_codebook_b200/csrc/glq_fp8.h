@@ -144,6 +144,9 @@ struct MoeParams {
     unsigned *err;
 };
 int moe_tile(int T);
+// the kernel's grid barrier, all its CTAs arriving or all but one
+cudaError_t launch_moe_wait_selftest(uint64_t *bar, unsigned *err, int grid, bool all, unsigned long long limit,
+                                     cudaStream_t s);
 // cooperative: `grid` CTAs, one per SM
 cudaError_t launch_moe(const MoeParams &p, int grid, cudaStream_t s);
 

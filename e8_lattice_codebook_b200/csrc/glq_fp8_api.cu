@@ -574,6 +574,13 @@ glq_status glq_moe_check(glq_moe L, void *stream) {
     return glq::take_error(L->d_err, static_cast<cudaStream_t>(stream), L->d_bar);
 }
 
+glq_status glq_moe_selftest_wait(glq_moe L, int arrivals, int64_t limit, void *stream) {
+    if (!L || arrivals < 1 || arrivals > 2 || limit <= 0) return GLQ_ERR_INVALID_ARG;
+    DeviceGuard guard(L->device);
+    return launched(glq::launch_moe_wait_selftest(L->d_bar, L->d_err, L->num_sms, arrivals == 2, (unsigned long long)limit,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
 glq_status glq_moe_info(glq_moe L, glq_moe_config *config, size_t *device_bytes) {
     if (!L) return GLQ_ERR_INVALID_ARG;
     if (config)

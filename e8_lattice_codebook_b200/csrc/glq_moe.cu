@@ -136,17 +136,6 @@ __device__ __forceinline__ void route(const MoeParams &p, int t, int lane, int16
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-__device__ __forceinline__ uint64_t atom_add_u64(uint64_t *p, uint64_t v) {
-    uint64_t old;
-    asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(old) : "l"(p), "l"(v) : "memory");
-    return old;
-}
-__device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t *p) {
-    uint64_t v;
-    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 
 __device__ __forceinline__ float silu(float v) { return v / (1.f + expf(-v)); }
@@ -279,16 +268,7 @@ __device__ __forceinline__ void moe_body(const MoeParams &p, const Routing &z, B
             uint64_t *const mine[4] = {&bars.part0, &bars.part1, &bars.formed, &bars.part2};
             for (int n = LOCAL ? 1 : 0; n < 4; n += LOCAL ? 2 : 1) {
                 if (!pipe.wait(mine[n], 0, p.err)) break;
-                // release: what this CTA's warps wrote before they arrived
-                const uint64_t old = atom_add_u64(p.bar, 1);
-                const uint64_t target = (old / G + 1) * G;  // every call adds a multiple of G
-                const uint64_t t0 = sm100::clock_cycles();
-                bool ok = true;
-                while (ok && ld_acquire_u64(p.bar) < target) {
-                    if (pipe.abort) ok = false;
-                    else if (sm100::clock_cycles() - t0 > WAIT_CYCLES) pipe.fail(p.err), ok = false;
-                }
-                if (!ok) break;
+                if (!grid_barrier(p.bar, G, &pipe.abort, p.err)) break;
                 sm100::mbar_arrive(&bars.grid[n]);
             }
         }

@@ -52,7 +52,23 @@ __global__ void fp8_wait_selftest_kernel(unsigned *err, int arrivals, unsigned l
     else if (ran_out[0]) atomicOr(err, ran_out[0]);
 }
 
+// The experts' grid barrier over G CTAs, of which the launch has G or one less.
+__global__ void moe_wait_selftest_kernel(uint64_t *bar, unsigned *err, uint32_t G, unsigned long long limit) {
+    __shared__ volatile int abort;
+    if (threadIdx.x != 0) return;
+    abort = 0;
+    fp8::grid_barrier(bar, G, &abort, err, limit);
+}
+
 }  // namespace
+
+cudaError_t launch_moe_wait_selftest(uint64_t *bar, unsigned *err, int grid, bool all, unsigned long long limit,
+                                     cudaStream_t s) {
+    uint32_t G = grid;
+    void *args[] = {&bar, &err, &G, &limit};
+    return cudaLaunchCooperativeKernel((const void *)moe_wait_selftest_kernel, dim3(all ? grid : grid - 1), dim3(32), args,
+                                       0, s);
+}
 
 cudaError_t launch_fp8_wait_selftest(unsigned *err, int arrivals, unsigned long long limit, cudaStream_t s) {
     fp8_wait_selftest_kernel<<<1, 64, 0, s>>>(err, arrivals, limit);

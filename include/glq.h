@@ -637,8 +637,23 @@ GLQ_API glq_status glq_moe_reserve(glq_moe layer, int64_t max_T);
 GLQ_API glq_status glq_moe_forward(glq_moe layer, const void *x_dev, glq_dtype x_dtype, const void *logits_dev,
                                    glq_dtype logits_dtype, void *y_dev, glq_dtype y_dtype, int64_t T, void *stream);
 
-/* glq_moe_check -- glq_layer_check for this layer. */
+/*
+ * glq_moe_check -- glq_layer_check for this layer.  After GLQ_ERR_TIMEOUT the
+ * results of every call since the last check are void: a call that gave up may
+ * leave the barrier between its CTAs half way, and the calls after it then
+ * pass it too early or give up themselves.  The check clears it, so no call of
+ * this layer may be under way on another stream.
+ */
 GLQ_API glq_status glq_moe_check(glq_moe layer, void *stream);
+
+/*
+ * glq_moe_selftest_wait -- glq_layer_selftest_wait for the bounded wait of the
+ * barrier between this layer's CTAs (limit in SM clock cycles): at arrivals 1
+ * one CTA never arrives, at 2 all do.  The barrier is the layer's own: after a
+ * timeout glq_moe_check has to come before the next call.  Errors:
+ * GLQ_ERR_INVALID_ARG, GLQ_ERR_CUDA.  Asynchronous.
+ */
+GLQ_API glq_status glq_moe_selftest_wait(glq_moe layer, int arrivals, int64_t limit, void *stream);
 
 /* Layer geometry.  Any output may be NULL. */
 GLQ_API glq_status glq_moe_info(glq_moe layer, glq_moe_config *config, size_t *device_bytes);

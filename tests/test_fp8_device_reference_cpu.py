@@ -1,5 +1,5 @@
 """The 64-bit definitions that run on a device, on the CPU against those of
-fp8_reference.py; their checker, and the plan entry's refusals."""
+fp8_reference.py; their checker, and the refusals of the test entries."""
 import numpy as np
 import pytest
 import torch
@@ -59,8 +59,9 @@ def test_sigmoid_weights_far_below_zero():
     np.testing.assert_allclose(w.numpy(), [[1 / (1 + np.exp(-1)), 1 / (1 + np.e)]], rtol=1e-12)
 
 
-def test_plan_refusals():
+def test_null_handles():
     from e8_lattice_codebook_b200 import build as glq_build
     glq_build.build()
     import e8_lattice_codebook_b200 as glq
     assert glq._L().glq_fp8_plan(None, 1, None, None, None, None, None) == 1
+    assert glq._L().glq_moe_selftest_wait(None, 1, 10, None) == 1
