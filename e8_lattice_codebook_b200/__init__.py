@@ -543,8 +543,10 @@ class GlqLinear:
         B = x.shape[0]
         odt = out_dtype or x.dtype
         if out is None:
-            out = _empty((B, self.m), odt, x.device, stream)
-        _used_on(stream, x, out)
+            out = (torch.empty((B, self.m), dtype=odt, device=x.device) if stream is None
+                   else _empty((B, self.m), odt, x.device, stream))
+        if stream is not None:
+            _used_on(stream, x, out)
         glq_linear(self.handle, x.data_ptr(), dtype_code(x.dtype), out.data_ptr(),
                    dtype_code(out.dtype), B, _stream_ptr(stream))
         return out
