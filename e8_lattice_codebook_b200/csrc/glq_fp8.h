@@ -71,8 +71,9 @@ constexpr int FP8_ROUND_FEW = 4, FP8_ROUND_MAX = 8;  // most tokens of sources 0
 // whether the few-token kernel rounds f16 / bf16 activations itself (sources 0
 // and 1); else the quantiser runs first
 bool fp8_rounds_inside(int64_t B, int64_t tiles, int KB, int num_sms);
-// Most tokens of the few-token kernel.  4096x14336 takes 19.8 us at 64 tokens
-// (few) and 27.1 at 65 (many); as two few-token calls 65 would take 35.
+// Most tokens of the few-token kernel.  4096x14336 takes 19.5 us at 64 tokens
+// (few) and 27.1 at 65 (many), the quantiser included; as two few-token calls of
+// 64 and 1, 65 would take 32.
 constexpr int FP8_FEW = 64;
 int fp8_skinny_tile(int64_t B);  // NT: tokens per tile for a batch of B <= FP8_FEW
 // clusters of c = 1..8 CTAs (one per SM) the current device holds at once

@@ -526,7 +526,8 @@ GLQ_API glq_status glq_fp8_reserve(glq_fp8 layer, int64_t max_B);
  * x_dev: device [B][n] (GLQ_F16 or GLQ_BF16), y_dev: device [B][m] (x's dtype
  * or GLQ_F32), both row-major and 16-byte aligned.  B >= 0 (0 is a no-op).
  * Paths: up to 64 tokens a kernel bound by reading the weights, whose clusters
- *   split K (it rounds up to 4 tokens itself; above, a kernel before it does);
+ *   split K (it rounds up to 4 tokens itself, in small layers up to 8; above, a
+ *   kernel before it does);
  *   above 64 a tcgen05 GEMM of CTA pairs, which splits K through the shared
  *   workspace when the output has few tiles.  A batch of more than 8192 runs
  *   8192 at a time.  A call's results are the same bits run to run; between
