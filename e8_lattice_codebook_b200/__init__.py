@@ -467,6 +467,12 @@ def _stream_ptr(stream):
     return s.cuda_stream
 
 
+def _torch_stream(stream, device):
+    """A stream as torch's own object: any that has a `cuda_stream` is taken."""
+    cuda = _torch().cuda
+    return stream if isinstance(stream, cuda.Stream) else cuda.ExternalStream(stream.cuda_stream, device=device)
+
+
 def _empty(shape, dtype, device, stream):
     """A call's result, allocated on the stream that will write it: a block of
     the current stream's could still be read by work queued there, which a
@@ -478,7 +484,7 @@ def _empty(shape, dtype, device, stream):
     current = torch.cuda.current_stream(device)
     if stream.cuda_stream == current.cuda_stream:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream, device)):
         out = torch.empty(shape, dtype=dtype, device=device)
     out.record_stream(current)
     return out
@@ -487,6 +493,7 @@ def _empty(shape, dtype, device, stream):
 def _used_on(stream, *tensors):
     """Tensors that a call on `stream` reads or writes stay while it does."""
     if stream is not None and stream.cuda_stream != _torch().cuda.current_stream(tensors[0].device).cuda_stream:
+        stream = _torch_stream(stream, tensors[0].device)
         for t in tensors:
             t.record_stream(stream)
 
@@ -662,8 +669,8 @@ def _call_stream(index, stream, *tensors):
     current = _raw_stream(index)
     if stream is None or stream.cuda_stream == current:
         return current
-    for t in tensors:
-        t.record_stream(stream)
+    if tensors:
+        _used_on(stream, *tensors)
     return stream.cuda_stream
 
 

@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import _empty, _stream_ptr, _torch, _used_on, dtype_code, glq_cast, glq_layer_create_shard, \
+from . import _empty, _stream_ptr, _torch, _torch_stream, _used_on, dtype_code, glq_cast, glq_layer_create_shard, \
     glq_layer_destroy, glq_linear
 
 CHUNK = 128
@@ -64,6 +64,7 @@ class RowParallelLinear:
         if stream is not None:
             # the collective waits for the current stream and is waited for there
             current = torch.cuda.current_stream(x.device)
+            stream = _torch_stream(stream, x.device)
             with torch.cuda.stream(stream):
                 y = self(x, out_dtype)
             if stream.cuda_stream != current.cuda_stream:

@@ -46,8 +46,9 @@ def _check(call):
     want = call(None).clone()
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
-    assert torch.equal(call(side), want)  # loads what it needs
+    got = call(side)  # loads what it needs
     torch.cuda.synchronize()
+    assert torch.equal(got, want)
     for _ in range(3):
         # a block that the current stream has yet to read, given back to the allocator
         block = torch.full_like(want, 3)
@@ -83,3 +84,32 @@ def test_lattice_results(glq):
     _check(lambda st: layer(x[:2], out_dtype=torch.float32, stream=st))
     _check(lambda st: layer.dequant(stream=st))
     _check(lambda st: layer.rht_input(x, stream=st))
+
+
+def test_captured_on_a_given_stream(glq):
+    """Calls on a stream that was forked from the capturing one, their results dropped while capturing or kept."""
+    gen = torch.Generator("cuda").manual_seed(63)
+    x = torch.randn(24, 264, generator=gen, device="cuda").to(torch.bfloat16)
+    linear = glq.Fp8Linear(*ref.random_weight(gen, 264, 264))
+    L = gi.make_layer(63, 0, 256, 264, 2)
+    lattice = Device().layer(L)
+    linear.reserve(24)
+    lattice.reserve(24)
+    want = lattice(linear(linear(x)))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        linear(x, stream=side)
+        q, s = glq.fp8_quantize(linear(x, stream=side), stream=side)
+        y = lattice(linear.forward_quantized(q, s, stream=side), stream=side)
+        del q, s
+        torch.cuda.current_stream().wait_stream(side)
+        z = y + 0
+    for _ in range(3):
+        x.copy_(torch.randn_like(x))
+        want = lattice(linear(linear(x)))
+        graph.replay()
+        assert torch.equal(y, want) and torch.equal(z, want)
+    torch.cuda.synchronize()

@@ -54,7 +54,8 @@ class World:
             world.now = before
 
         self.Tensor = Tensor
-        cuda = types.SimpleNamespace(current_device=lambda: 0, current_stream=lambda d=None: world.now, stream=stream,
+        cuda = types.SimpleNamespace(Stream=Stream, ExternalStream=lambda raw, device: {1: self.main, 2: self.side}[raw],
+                                     current_device=lambda: 0, current_stream=lambda d=None: world.now, stream=stream,
                                      device=lambda i: contextlib.nullcontext())
         self.torch = types.SimpleNamespace(
             cuda=cuda, float16=torch.float16, bfloat16=torch.bfloat16, device=torch.device, float32=torch.float32, float8_e4m3fn=torch.float8_e4m3fn,
@@ -103,7 +104,8 @@ CALLS = ["quantize", "linear", "linear, f32", "quantized", "dequant", "moe"]
 
 def _check(w, calls, name):
     run, inputs, dtypes = calls[name]
-    for given, other in ((w.side, True), (w.main, False), (None, False)):
+    bare = types.SimpleNamespace(cuda_stream=2)  # another library's
+    for given, other in ((w.side, True), (bare, True), (w.main, False), (None, False)):
         for t in inputs:
             t.recorded.clear()
         w.launches.clear()
@@ -112,7 +114,7 @@ def _check(w, calls, name):
         assert [o.dtype for o in outs] == dtypes
         assert w.launches == [(given or w.main).cuda_stream]
         for o in outs:
-            assert o.on is (given or w.main), name
+            assert o.on is (w.side if other else w.main), name
             assert (w.main in o.recorded) == other
         for t in inputs:
             assert (w.side in t.recorded) == other
