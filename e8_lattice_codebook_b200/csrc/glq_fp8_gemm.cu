@@ -138,7 +138,9 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
 
     // CTA scope: what the barriers order is copies, MMAs and TMEM loads (the
     // tcgen05 fences), no stores of another CTA.  Cluster-scope acquires, one
-    // per drain warp and K block, cost more than the K block's MMAs.
+    // per drain warp and K block, cost more than the K block's MMAs; on the MMA
+    // thread's waits for accumulators alone 4096x14336 with 2048 tokens took 257
+    // us instead of 140.
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bounded(bar, parity, &abort_flag, p.err); };
     const int KB = p.KB, items = p.tiles * p.ksplit;
     // an item: a tile's token and weight-row place and its share of the K blocks
