@@ -1,5 +1,5 @@
 """The 64-bit definitions that run on a device, on the CPU against those of
-fp8_reference.py; their checker, and the refusals of the test entries."""
+fp8_reference.py; their comparison, and the refusals of the test entries."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +8,7 @@ import fp8_device_reference as dev
 import fp8_reference as ref
 
 
-def test_checker_refuses_nan_and_values_outside():
+def test_comparison_refuses_nan_and_values_outside():
     want = torch.tensor([1.0, -2.0, 0.0, 5.0, 5.0], dtype=torch.float64)
     bound = torch.tensor([0.5, 0.5, 0.0, 0.25, 0.25], dtype=torch.float64)
     got = torch.tensor([1.5, float("nan"), 0.0, 5.25 + 2.0 ** -20, float("inf")])
